@@ -54,8 +54,9 @@ typedef enum kronq_status {
   KRONQ_ERR_TIMEOUT = 7       /* a kernel gave up a bounded wait (see kronq_device_error) */
 } kronq_status;
 
-/* Element types of the weight input of kronq_biip. */
-enum { KRONQ_DTYPE_BF16 = 0, KRONQ_DTYPE_F32 = 1 };
+/* Element types. Floating inputs and outputs are BF16 or F32; the weight codes of the 8-bit
+ * calls are U8 or S8. */
+enum { KRONQ_DTYPE_BF16 = 0, KRONQ_DTYPE_F32 = 1, KRONQ_DTYPE_U8 = 2, KRONQ_DTYPE_S8 = 3 };
 
 /* Flags of kronq_biip ([KronQ-hyper] Method, BiIP equations). */
 enum {
@@ -82,9 +83,9 @@ KRONQ_API kronq_status kronq_device_check(void);
 KRONQ_API uint64_t kronq_launch_count(void);
 
 /* SM budget for the persistent kernels (the statistics kernel of kronq_accumulate and the
- * tensor-core GEMMs inside kronq_cholinv and kronq_quantize_layer): launches made while a budget
- * of n > 0 is set use at most n CTAs, one per SM, so that work on other streams keeps the rest
- * of the GPU. 0 (the default) lifts it. Process-wide, read at launch time (a captured CUDA graph
+ * tensor-core GEMMs inside kronq_cholinv, kronq_quantize_layer and kronq_matmul_i8): launches
+ * made while a budget of n > 0 is set use at most n CTAs, one per SM, so that work on other
+ * streams keeps the rest of the GPU. 0 (the default) lifts it. Process-wide, read at launch time (a captured CUDA graph
  * keeps the grid it was captured with); it changes no result. Not a reservation: nothing stops
  * other kernels from using the budgeted SMs. */
 KRONQ_API void kronq_set_sm_budget(int32_t sms);
@@ -396,6 +397,119 @@ KRONQ_API kronq_status kronq_qlinear(const void* x, int32_t x_dtype, int64_t ld_
                                      uint32_t flags, int32_t d_out, int32_t d_in, int32_t bits,
                                      float* y, int64_t ld_y, void* workspace,
                                      size_t workspace_bytes, kronq_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------
+ * 7. The quantized layer in 8-bit integers (any code width the solve gives, any token count).
+ *
+ * kronq_qlinear reads packed 2/3/4-bit codes and at most 32 tokens a pass. These calls take the
+ * solve's codes as they are (one byte each, 2..8 bits, one grid per row) and quantize the
+ * activations to 8 bits per token, so that the product runs on the integer tensor cores:
+ *     x'_t = V S_X^-1 x_t,  s_t = max_j |x'_tj| / 127,  q_tj = rint(x'_tj / s_t),
+ *     y'_to = s_t s_o (sum_i q_ti c_oi - z_o sum_i q_ti),  y = S_G^-1 U^T y'.
+ * Byte matrices (q, codes) are row-major with a 16-byte aligned base and a row stride that is a
+ * multiple of 16 bytes (the stride of a matrix of one row is not looked at).
+ * ------------------------------------------------------------------------------------- */
+/* kronq_quantize_tokens - 8-bit codes, scale and code sum of every token.
+ *
+ *   x        (device) n_tok x d_in, x_dtype KRONQ_DTYPE_BF16 or KRONQ_DTYPE_F32, row stride ld_x
+ *            elements (>= d_in), aligned to its element size; n_tok = 0 is a no-op
+ *   flags    KRONQ_BIIP_SCALE_IN (x / s_x) and KRONQ_BIIP_ROTATE_IN (signs, then Hadamard blocks
+ *            of the largest power of two in d_in); a flag that is off drops its factor and its
+ *            pointer may be NULL. d_in <= 65536, with ROTATE_IN <= 53248 (KRONQ_ERR_UNSUPPORTED)
+ *   q        (device, int8) n_tok x d_in, row stride ld_q bytes; bytes past d_in stay as they are
+ *   tok_scale (device, fp32), tok_sum (device, int32): n_tok each
+ *   Arithmetic: x' in fp32; s_t = max|x'| / 127 rounded once; q is the exact quotient x' / s_t
+ *   rounded to the nearest integer, ties to even, so |q| <= 127. A token whose s_t would be below
+ *   2^-126 (all zero, say) has q = 0, s_t = 1. A token with an infinity or a NaN in x' has q = 0
+ *   and s_t = NaN, which makes its whole output row NaN. */
+KRONQ_API kronq_status kronq_quantize_tokens(const void* x, int32_t x_dtype, int64_t ld_x,
+                                             int32_t n_tok, int32_t d_in, const float* s_x,
+                                             const int8_t* sign_in, uint32_t flags, int8_t* q,
+                                             int64_t ld_q, float* tok_scale, int32_t* tok_sum,
+                                             kronq_stream_t stream);
+
+/* kronq_matmul_i8 - y = s_t s_o (q c^T - z_o sum_t), the product in 8-bit integers.
+ *
+ *   q        (device, int8) n_tok x d_in token codes, row stride ld_q; tok_scale (fp32) and
+ *            tok_sum (int32, the row sums of q; may be NULL when zero is NULL): n_tok each
+ *   codes    (device) d_out x d_in weight codes, codes_dtype KRONQ_DTYPE_U8 or KRONQ_DTYPE_S8, row
+ *            stride ld_codes
+ *   scale, zero (device, fp32) d_out each, as kronq_quantize_layer gives them with group 0; zero
+ *            may be NULL (no zero point, symmetric codes)
+ *   y        (device) n_tok x d_out, y_dtype KRONQ_DTYPE_F32 or KRONQ_DTYPE_BF16, row stride ld_y
+ *            elements (>= d_out), aligned to its element size
+ *   d_in <= 65536 (the int32 sums are then exact). n_tok = 0 is a no-op. No workspace.
+ *   Arithmetic: the integer sum and its zero-point correction are exact (for a zero that is no
+ *   whole number, or so large that int32 could not hold the result, in fp64); it is rounded to
+ *   fp32, multiplied by fl(s_t s_o) and rounded to y's type. Deterministic. */
+KRONQ_API kronq_status kronq_matmul_i8(const int8_t* q, int64_t ld_q, const float* tok_scale,
+                                       const int32_t* tok_sum, int32_t n_tok, const void* codes,
+                                       int32_t codes_dtype, int64_t ld_codes, const float* scale,
+                                       const float* zero, int32_t d_out, int32_t d_in, void* y,
+                                       int32_t y_dtype, int64_t ld_y, kronq_stream_t stream);
+
+/* kronq_qlinear8 - y = S_G^-1 U^T W^' V S_X^-1 x in 8-bit integers, for any number of tokens.
+ *
+ *   The arguments of the two calls above; s_x, s_g, sign_in, sign_out, flags as for kronq_qlinear
+ *   (Hadamard blocks of the output up to 16384). The transforms are applied in fp32, y is rounded
+ *   once. workspace: kronq_qlinear8_workspace_size(n_tok, d_out, d_in, flags) bytes; it does not
+ *   grow past 16384 tokens (2048 with ROTATE_OUT), which are then taken in turn. */
+KRONQ_API size_t kronq_qlinear8_workspace_size(int32_t n_tok, int32_t d_out, int32_t d_in,
+                                               uint32_t flags);
+KRONQ_API kronq_status kronq_qlinear8(const void* x, int32_t x_dtype, int64_t ld_x, int32_t n_tok,
+                                      const void* codes, int32_t codes_dtype, int64_t ld_codes,
+                                      const float* scale, const float* zero, const float* s_x,
+                                      const float* s_g, const int8_t* sign_in,
+                                      const int8_t* sign_out, uint32_t flags, int32_t d_out,
+                                      int32_t d_in, void* y, int32_t y_dtype, int64_t ld_y,
+                                      void* workspace, size_t workspace_bytes,
+                                      kronq_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------
+ * 8. Distillation from a teacher's top logits: the loss and the gradient of the logits.
+ *
+ * [KronQ-hyper] Method takes g = dL/dy from a backward pass of the model over the calibration
+ * tokens; these calls give that pass its loss, with the full-precision model as the teacher and
+ * the (partly) quantized one as the student. dlogits in bf16 is an input of kronq_accumulate (the
+ * G of the output head). Per token, with temperature tau and the teacher's entries (id_j, t_j):
+ *     p_j = exp(t_j / tau - L),  L = logsumexp_j(t_j / tau), or top_lse (then sum p_j <= 1 is the
+ *           mass of the listed entries under the teacher's whole distribution)
+ *     lse = logsumexp_v(z_v / tau),  loss = w tau^2 sum_j p_j (log p_j - z[id_j] / tau + lse)
+ *     dloss/dz_v = w tau (P q_v - sum_{j: id_j = v} p_j),  P = sum_j p_j, q_v = exp(z_v / tau - lse)
+ *
+ *   logits   (device) n_tok x vocab student logits z, logits_dtype BF16 or F32, row stride
+ *            ld_logits elements, aligned to the element size. -inf entries have q = 0 (a listed
+ *            one makes the loss +inf); +inf and NaN make their row NaN
+ *   ids      (device, int32) n_tok x k, row stride ld_ids; an id outside 0 .. vocab - 1 (-1, say)
+ *            marks an absent entry, whose logit is not used; an id listed twice counts twice
+ *   top      (device) n_tok x k teacher logits t, top_dtype BF16 or F32, row stride ld_top. -inf
+ *            entries count nothing
+ *   k        0 .. 1024; rows without any entry have loss 0 and gradient 0
+ *   top_lse  (device, fp32, n_tok) or NULL; row_weight w (device, fp32, n_tok) or NULL (1). A row
+ *            of weight 0 has loss 0 and gradient 0 whatever its logits hold
+ *   temperature tau, in [1e-4, 1e4]
+ *   loss     (device, fp32, n_tok); lse (device, fp32, n_tok) or NULL
+ *   dlogits  (device) n_tok x vocab, dlogits_dtype BF16 or F32, row stride ld_dlogits, or NULL (the
+ *            loss alone). It may be logits itself (same type and stride), not overlap it otherwise
+ *   n_tok = 0 is a no-op. Sums and softmax statistics in fp32 or fp64. Deterministic.
+ * kronq_distill_backward gives the gradient alone, from lse (as kronq_distill returned it) and the
+ * upstream gradient dloss (device, fp32, n_tok), which takes the place of w.
+ * ------------------------------------------------------------------------------------- */
+KRONQ_API kronq_status kronq_distill(const void* logits, int32_t logits_dtype, int64_t ld_logits,
+                                     const int32_t* ids, int64_t ld_ids, const void* top,
+                                     int32_t top_dtype, int64_t ld_top, int32_t n_tok,
+                                     int32_t vocab, int32_t k, const float* top_lse,
+                                     const float* row_weight, float temperature, float* loss,
+                                     float* lse, void* dlogits, int32_t dlogits_dtype,
+                                     int64_t ld_dlogits, kronq_stream_t stream);
+KRONQ_API kronq_status kronq_distill_backward(const void* logits, int32_t logits_dtype,
+                                              int64_t ld_logits, const int32_t* ids,
+                                              int64_t ld_ids, const void* top, int32_t top_dtype,
+                                              int64_t ld_top, int32_t n_tok, int32_t vocab,
+                                              int32_t k, const float* top_lse, const float* lse,
+                                              const float* dloss, float temperature,
+                                              void* dlogits, int32_t dlogits_dtype,
+                                              int64_t ld_dlogits, kronq_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -782,3 +782,88 @@ def score_allocate(tr_hx, tr_hg, n_params, choices, avg_bits):
                 bits[l] = b
                 break
     return s, bits
+
+
+# ------------------------------------------------------------------ the layer in 8-bit integers
+
+def quantize_tokens(x, s_x=None, sign_in=None):
+    """(x', s, q, sum) of each token: x' = V S_X^-1 x, s = fp32(max |x'| / 127), q = rint(x' / s).
+
+    s = 1, q = 0 where max |x'| / 127 is below 2^-126; s = NaN, q = 0 where x' is not finite.
+    """
+    xp = np.asarray(x, dtype=np.float64)
+    if s_x is not None:
+        xp = xp / np.asarray(s_x, dtype=np.float64)[None, :]
+    if sign_in is not None:
+        xp = hadamard_rows(xp * np.asarray(sign_in, dtype=np.float64)[None, :])
+    with np.errstate(invalid="ignore"):
+        finite = np.isfinite(xp).all(axis=1)
+        s = (np.abs(xp).max(axis=1) / 127.0).astype(np.float32).astype(np.float64)
+        zero = s < 2.0 ** -126
+        s = np.where(finite, np.where(zero, 1.0, s), np.nan)
+        q = np.where((finite & ~zero)[:, None], np.rint(xp / s[:, None]), 0.0).astype(np.int64)
+    return xp, s, q, q.sum(axis=1)
+
+
+def hadamard_rows(x):
+    """Orthonormal Hadamard transform of each aligned block (largest power of two in the width)."""
+    n, d = x.shape
+    b = hadamard_block_size(d)
+    v = x.reshape(n, d // b, b)
+    h = 1
+    while h < b:
+        v = v.reshape(n, d // b, b // (2 * h), 2, h)
+        v = np.concatenate([(v[..., 0, :] + v[..., 1, :])[..., None, :],
+                            (v[..., 0, :] - v[..., 1, :])[..., None, :]], axis=-2)
+        h *= 2
+    return v.reshape(n, d) / np.sqrt(float(b))
+
+
+def matmul_i8(q, tok_scale, codes, scale, zero=None):
+    """s_t s_o sum_i q_ti (c_oi - z_o), the integer part exact."""
+    c = np.asarray(codes, dtype=np.float64)
+    if zero is not None:
+        c = c - np.asarray(zero, dtype=np.float64)[:, None]
+    y = np.asarray(q, dtype=np.float64) @ c.T
+    return y * np.asarray(tok_scale, dtype=np.float64)[:, None] * \
+        np.asarray(scale, dtype=np.float64)[None, :]
+
+
+# --------------------------------------------------------- distillation from top logits
+
+def distill(z, ids, top, tau=1.0, top_lse=None, weight=None, lse=None):
+    """(loss, lse, gradient) per token, entry by entry from the definition."""
+    z = np.asarray(z, dtype=np.float64)
+    n, v = z.shape
+    w = np.ones(n) if weight is None else np.asarray(weight, dtype=np.float64)
+    loss, out_lse, grad = np.zeros(n), np.zeros(n), np.zeros((n, v))
+    for r in range(n):
+        u = z[r] / tau
+        m = u.max()
+        l = m + math.log(np.exp(u - m).sum()) if np.isfinite(m) else m
+        l = l if lse is None else float(lse[r])
+        out_lse[r] = l
+        q = np.exp(u - l) if np.isfinite(l) else np.zeros(v)
+        listed = [(int(i), float(t) / tau) for i, t in zip(ids[r], top[r]) if 0 <= int(i) < v]
+        if w[r] == 0.0:
+            continue
+        if top_lse is None:
+            ts = [t for _, t in listed if t != -math.inf]
+            if not ts:
+                continue
+            mt = max(ts)
+            lt = mt + math.log(math.fsum(math.exp(t - mt) for t in ts))
+        else:
+            lt = float(top_lse[r])
+        mass = 0.0
+        for i, t in listed:
+            lp = t - lt
+            p = math.exp(lp) if lp != -math.inf else 0.0
+            if p > 0.0:
+                loss[r] += p * (lp - u[i] + l) if u[i] != -math.inf else math.inf
+            grad[r, i] -= p
+            mass += p
+        grad[r] += mass * q
+        loss[r] *= w[r] * tau * tau
+        grad[r] *= w[r] * tau
+    return loss, out_lse, grad

@@ -138,6 +138,116 @@ kronq_status check_bf16_matrix(const void* p, int64_t ld, int cols, const char* 
   return KRONQ_OK;
 }
 
+bool float_dtype(int32_t t) { return t == KRONQ_DTYPE_BF16 || t == KRONQ_DTYPE_F32; }
+int dtype_bytes(int32_t t) { return t == KRONQ_DTYPE_BF16 ? 2 : 4; }
+
+// A float matrix of the calls that take either type at any stride.
+kronq_status check_float_matrix(const void* p, int32_t dtype, int64_t ld, int64_t rows,
+                                int64_t cols, const char* name) {
+  if (!float_dtype(dtype))
+    return fail(KRONQ_ERR_INVALID_ARG, "%s: type must be KRONQ_DTYPE_BF16 or KRONQ_DTYPE_F32", name);
+  if (!p) return fail(KRONQ_ERR_INVALID_ARG, "%s is NULL", name);
+  if (!aligned(p, dtype_bytes(dtype)))
+    return fail(KRONQ_ERR_INVALID_ARG, "%s not aligned to its element size", name);
+  if (rows > 1 && ld < cols)
+    return fail(KRONQ_ERR_SHAPE, "%s: stride %lld < width %lld", name, (long long)ld,
+                (long long)cols);
+  return KRONQ_OK;
+}
+
+// A byte matrix that tensor copies read; the stride of a single row is replaced by a valid one.
+kronq_status check_byte_matrix(const void* p, int64_t* ld, int64_t rows, int64_t cols,
+                               const char* name) {
+  if (!p) return fail(KRONQ_ERR_INVALID_ARG, "%s is NULL", name);
+  if (!aligned(p, 16)) return fail(KRONQ_ERR_INVALID_ARG, "%s not 16-byte aligned", name);
+  if (rows == 1) *ld = (cols + 15) / 16 * 16;
+  if (*ld < cols)
+    return fail(KRONQ_ERR_SHAPE, "%s: stride %lld < width %lld", name, (long long)*ld,
+                (long long)cols);
+  if (*ld % 16 != 0)
+    return fail(KRONQ_ERR_INVALID_ARG, "%s: stride %lld is not a multiple of 16 bytes", name,
+                (long long)*ld);
+  return KRONQ_OK;
+}
+
+kronq_status check_quant_tokens(const void* x, int32_t x_dtype, int64_t ld_x, int32_t n_tok,
+                                int32_t d_in, const float* s_x, const int8_t* sign_in,
+                                uint32_t flags) {
+  KQ_TRY(check_float_matrix(x, x_dtype, ld_x, n_tok, d_in, "x"));
+  if ((flags & KRONQ_BIIP_SCALE_IN) && !s_x) return fail(KRONQ_ERR_INVALID_ARG, "s_x is NULL");
+  if ((flags & KRONQ_BIIP_ROTATE_IN) && !sign_in)
+    return fail(KRONQ_ERR_INVALID_ARG, "sign_in is NULL");
+  if (d_in > kMaxI8Width)
+    return fail(KRONQ_ERR_UNSUPPORTED, "d_in = %d exceeds %d", d_in, kMaxI8Width);
+  if ((flags & KRONQ_BIIP_ROTATE_IN) && d_in > kMaxRotatedWidth)
+    return fail(KRONQ_ERR_UNSUPPORTED, "d_in = %d exceeds %d, the widest rotated token", d_in,
+                kMaxRotatedWidth);
+  return KRONQ_OK;
+}
+
+kronq_status check_codes(const void* codes, int32_t codes_dtype, int64_t* ld_codes,
+                         const float* scale, const float* zero, int32_t d_out, int32_t d_in) {
+  if (codes_dtype != KRONQ_DTYPE_U8 && codes_dtype != KRONQ_DTYPE_S8)
+    return fail(KRONQ_ERR_INVALID_ARG, "codes_dtype must be KRONQ_DTYPE_U8 or KRONQ_DTYPE_S8");
+  KQ_TRY(check_byte_matrix(codes, ld_codes, d_out, d_in, "codes"));
+  if (!scale) return fail(KRONQ_ERR_INVALID_ARG, "scale is NULL");
+  if (!aligned(scale, 4) || !aligned(zero, 4))
+    return fail(KRONQ_ERR_INVALID_ARG, "scale or zero not 4-byte aligned");
+  if (d_in > kMaxI8Width)
+    return fail(KRONQ_ERR_UNSUPPORTED, "d_in = %d exceeds %d", d_in, kMaxI8Width);
+  return KRONQ_OK;
+}
+
+// Workspace of kronq_qlinear8: [q][token scales][token sums][y' fp32, with an output rotation].
+// Tokens of one pass: an output rotation takes them 2048 at a time, so that y' stays small.
+struct Qlinear8Plan {
+  int chunk;
+  int64_t ld_q;
+  size_t q_bytes, tok_bytes, y_bytes;
+  size_t total() const { return q_bytes + 2 * tok_bytes + y_bytes; }
+};
+Qlinear8Plan qlinear8_plan(int32_t n_tok, int32_t d_out, int32_t d_in, uint32_t flags) {
+  const bool rot = (flags & KRONQ_BIIP_ROTATE_OUT) != 0;
+  Qlinear8Plan p;
+  p.chunk = std::min<int32_t>(n_tok, rot ? 2048 : 16384);
+  p.ld_q = (static_cast<int64_t>(d_in) + 15) / 16 * 16;
+  p.q_bytes = align256(static_cast<size_t>(p.chunk) * p.ld_q);
+  p.tok_bytes = align256(static_cast<size_t>(p.chunk) * 4);
+  p.y_bytes = rot ? align256(static_cast<size_t>(p.chunk) * d_out * sizeof(float)) : 0;
+  return p;
+}
+
+kronq_status check_distill(const void* logits, int32_t logits_dtype, int64_t ld_logits,
+                           const int32_t* ids, int64_t ld_ids, const void* top, int32_t top_dtype,
+                           int64_t ld_top, int32_t n_tok, int32_t vocab, int32_t k,
+                           float temperature, const void* dlogits, int32_t dlogits_dtype,
+                           int64_t ld_dlogits) {
+  KQ_TRY(check_float_matrix(logits, logits_dtype, ld_logits, n_tok, vocab, "logits"));
+  if (k > kMaxDistillTop)
+    return fail(KRONQ_ERR_UNSUPPORTED, "k = %d exceeds %d listed entries", k, kMaxDistillTop);
+  if (k > 0) {
+    KQ_TRY(check_float_matrix(top, top_dtype, ld_top, n_tok, k, "top"));
+    KQ_TRY(check_float_matrix(ids, KRONQ_DTYPE_F32, ld_ids, n_tok, k, "ids"));   // 4-byte entries
+  }
+  if (!(temperature >= 1e-4f && temperature <= 1e4f))
+    return fail(KRONQ_ERR_INVALID_ARG, "temperature must be in [1e-4, 1e4]");
+  if (dlogits) {
+    KQ_TRY(check_float_matrix(dlogits, dlogits_dtype, ld_dlogits, n_tok, vocab, "dlogits"));
+    auto extent = [&](int64_t ld, int32_t t) {
+      return static_cast<uintptr_t>(((n_tok - 1) * ld + vocab) * dtype_bytes(t));
+    };
+    const uintptr_t z0 = reinterpret_cast<uintptr_t>(logits);
+    const uintptr_t d0 = reinterpret_cast<uintptr_t>(dlogits);
+    const bool same = z0 == d0 && logits_dtype == dlogits_dtype &&
+                      (n_tok == 1 || ld_logits == ld_dlogits);
+    if (!same && z0 < d0 + extent(ld_dlogits, dlogits_dtype) &&
+        d0 < z0 + extent(ld_logits, logits_dtype))
+      return fail(KRONQ_ERR_INVALID_ARG,
+                  "dlogits overlaps logits without being the same matrix (type and stride)");
+  }
+  return KRONQ_OK;
+}
+
 constexpr int64_t kDriftChunk = 32768;   // tokens per fp16 conversion (workspace bound)
 
 size_t drift_ld(int d_in) { return static_cast<size_t>((d_in + 7) / 8 * 8); }
@@ -502,6 +612,148 @@ kronq_status kronq_qlinear(const void* x, int32_t x_dtype, int64_t ld_x, int32_t
   q.y = y;
   q.ld_y = ld_y;
   return run_qlinear(q, workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+// ----------------------------------------------------------------------------- 8-bit layer
+kronq_status kronq_quantize_tokens(const void* x, int32_t x_dtype, int64_t ld_x, int32_t n_tok,
+                                   int32_t d_in, const float* s_x, const int8_t* sign_in,
+                                   uint32_t flags, int8_t* q, int64_t ld_q, float* tok_scale,
+                                   int32_t* tok_sum, kronq_stream_t stream) {
+  if (d_in <= 0 || n_tok < 0) return fail(KRONQ_ERR_SHAPE, "d_in must be positive and n_tok >= 0");
+  if (flags & ~static_cast<uint32_t>(KRONQ_BIIP_SCALE_IN | KRONQ_BIIP_ROTATE_IN))
+    return fail(KRONQ_ERR_INVALID_ARG, "flags may only hold SCALE_IN and ROTATE_IN");
+  if (n_tok == 0) return KRONQ_OK;
+  KQ_TRY(check_quant_tokens(x, x_dtype, ld_x, n_tok, d_in, s_x, sign_in, flags));
+  KQ_TRY(check_byte_matrix(q, &ld_q, n_tok, d_in, "q"));
+  if (!tok_scale || !tok_sum)
+    return fail(KRONQ_ERR_INVALID_ARG, "tok_scale and tok_sum are required");
+  KQ_TRY(kronq_device_check());
+  const QuantTokensArgs a{x, x_dtype, ld_x, n_tok, d_in,
+                          (flags & KRONQ_BIIP_SCALE_IN) ? s_x : nullptr,
+                          (flags & KRONQ_BIIP_ROTATE_IN) ? sign_in : nullptr,
+                          q, ld_q, tok_scale, tok_sum};
+  return run_quant_tokens(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+kronq_status kronq_matmul_i8(const int8_t* q, int64_t ld_q, const float* tok_scale,
+                             const int32_t* tok_sum, int32_t n_tok, const void* codes,
+                             int32_t codes_dtype, int64_t ld_codes, const float* scale,
+                             const float* zero, int32_t d_out, int32_t d_in, void* y,
+                             int32_t y_dtype, int64_t ld_y, kronq_stream_t stream) {
+  if (d_out <= 0 || d_in <= 0 || n_tok < 0)
+    return fail(KRONQ_ERR_SHAPE, "d_out, d_in must be positive and n_tok >= 0");
+  if (n_tok == 0) return KRONQ_OK;
+  KQ_TRY(check_codes(codes, codes_dtype, &ld_codes, scale, zero, d_out, d_in));
+  KQ_TRY(check_byte_matrix(q, &ld_q, n_tok, d_in, "q"));
+  if (!tok_scale) return fail(KRONQ_ERR_INVALID_ARG, "tok_scale is NULL");
+  if (zero && !tok_sum) return fail(KRONQ_ERR_INVALID_ARG, "tok_sum is NULL (zero needs it)");
+  KQ_TRY(check_float_matrix(y, y_dtype, ld_y, n_tok, d_out, "y"));
+  KQ_TRY(kronq_device_check());
+  const I8MatmulArgs a{q, ld_q, tok_scale, tok_sum, n_tok, codes, ld_codes,
+                       codes_dtype == KRONQ_DTYPE_S8, scale, zero, nullptr, d_out, d_in, y,
+                       y_dtype, ld_y};
+  return run_i8matmul(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t kronq_qlinear8_workspace_size(int32_t n_tok, int32_t d_out, int32_t d_in, uint32_t flags) {
+  if (n_tok <= 0 || d_out <= 0 || d_in <= 0) return 0;
+  return qlinear8_plan(n_tok, d_out, d_in, flags).total();
+}
+
+kronq_status kronq_qlinear8(const void* x, int32_t x_dtype, int64_t ld_x, int32_t n_tok,
+                            const void* codes, int32_t codes_dtype, int64_t ld_codes,
+                            const float* scale, const float* zero, const float* s_x,
+                            const float* s_g, const int8_t* sign_in, const int8_t* sign_out,
+                            uint32_t flags, int32_t d_out, int32_t d_in, void* y, int32_t y_dtype,
+                            int64_t ld_y, void* workspace, size_t workspace_bytes,
+                            kronq_stream_t stream) {
+  if (d_out <= 0 || d_in <= 0 || n_tok < 0)
+    return fail(KRONQ_ERR_SHAPE, "d_out, d_in must be positive and n_tok >= 0");
+  if (flags & ~static_cast<uint32_t>(KRONQ_BIIP_FULL))
+    return fail(KRONQ_ERR_INVALID_ARG, "flags may only hold the four transform bits");
+  if (n_tok == 0) return KRONQ_OK;
+  KQ_TRY(check_quant_tokens(x, x_dtype, ld_x, n_tok, d_in, s_x, sign_in, flags));
+  KQ_TRY(check_codes(codes, codes_dtype, &ld_codes, scale, zero, d_out, d_in));
+  if ((flags & KRONQ_BIIP_SCALE_OUT) && !s_g) return fail(KRONQ_ERR_INVALID_ARG, "s_g is NULL");
+  const bool rot_out = (flags & KRONQ_BIIP_ROTATE_OUT) != 0;
+  if (rot_out && !sign_out) return fail(KRONQ_ERR_INVALID_ARG, "sign_out is NULL");
+  if (rot_out && (d_out & -d_out) > 16384)
+    return fail(KRONQ_ERR_UNSUPPORTED, "Hadamard blocks above 16384 are not supported");
+  KQ_TRY(check_float_matrix(y, y_dtype, ld_y, n_tok, d_out, "y"));
+  const Qlinear8Plan plan = qlinear8_plan(n_tok, d_out, d_in, flags);
+  KQ_TRY(check_ws(workspace, workspace_bytes, plan.total()));
+  KQ_TRY(kronq_device_check());
+
+  const float* scale_out = (flags & KRONQ_BIIP_SCALE_OUT) ? s_g : nullptr;
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  int8_t* q = reinterpret_cast<int8_t*>(w);
+  float* tok_scale = reinterpret_cast<float*>(w + plan.q_bytes);
+  int32_t* tok_sum = reinterpret_cast<int32_t*>(w + plan.q_bytes + plan.tok_bytes);
+  float* yp = reinterpret_cast<float*>(w + plan.q_bytes + 2 * plan.tok_bytes);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  for (int32_t t0 = 0; t0 < n_tok; t0 += plan.chunk) {
+    const int32_t n = std::min(plan.chunk, n_tok - t0);
+    const uint8_t* xt = static_cast<const uint8_t*>(x) + t0 * ld_x * dtype_bytes(x_dtype);
+    uint8_t* yt = static_cast<uint8_t*>(y) + t0 * ld_y * dtype_bytes(y_dtype);
+    const QuantTokensArgs qa{xt, x_dtype, ld_x, n, d_in,
+                             (flags & KRONQ_BIIP_SCALE_IN) ? s_x : nullptr,
+                             (flags & KRONQ_BIIP_ROTATE_IN) ? sign_in : nullptr,
+                             q, plan.ld_q, tok_scale, tok_sum};
+    KQ_TRY(run_quant_tokens(qa, s));
+    I8MatmulArgs ma{q, plan.ld_q, tok_scale, tok_sum, n, codes, ld_codes,
+                    codes_dtype == KRONQ_DTYPE_S8, scale, zero, rot_out ? nullptr : scale_out,
+                    d_out, d_in, yt, y_dtype, ld_y};
+    if (rot_out) {
+      ma.y = yp;
+      ma.y_dtype = KRONQ_DTYPE_F32;
+      ma.ld_y = d_out;
+    }
+    KQ_TRY(run_i8matmul(ma, s));
+    if (rot_out)
+      KQ_TRY(run_out_transform(yp, d_out, n, d_out, scale_out, sign_out, yt, y_dtype, ld_y, s));
+  }
+  return KRONQ_OK;
+}
+
+// ----------------------------------------------------------------------------- distillation
+kronq_status kronq_distill(const void* logits, int32_t logits_dtype, int64_t ld_logits,
+                           const int32_t* ids, int64_t ld_ids, const void* top, int32_t top_dtype,
+                           int64_t ld_top, int32_t n_tok, int32_t vocab, int32_t k,
+                           const float* top_lse, const float* row_weight, float temperature,
+                           float* loss, float* lse, void* dlogits, int32_t dlogits_dtype,
+                           int64_t ld_dlogits, kronq_stream_t stream) {
+  if (vocab <= 0 || n_tok < 0 || k < 0)
+    return fail(KRONQ_ERR_SHAPE, "vocab must be positive, n_tok and k >= 0");
+  if (n_tok == 0) return KRONQ_OK;
+  KQ_TRY(check_distill(logits, logits_dtype, ld_logits, ids, ld_ids, top, top_dtype, ld_top, n_tok,
+                       vocab, k, temperature, dlogits, dlogits_dtype, ld_dlogits));
+  if (!loss) return fail(KRONQ_ERR_INVALID_ARG, "loss is NULL");
+  KQ_TRY(kronq_device_check());
+  const DistillArgs a{logits, logits_dtype, ld_logits, ids, ld_ids, top, top_dtype, ld_top,
+                      n_tok, vocab, k, top_lse, row_weight, temperature, nullptr, loss, lse,
+                      dlogits, dlogits_dtype, ld_dlogits};
+  return run_distill(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+kronq_status kronq_distill_backward(const void* logits, int32_t logits_dtype, int64_t ld_logits,
+                                    const int32_t* ids, int64_t ld_ids, const void* top,
+                                    int32_t top_dtype, int64_t ld_top, int32_t n_tok,
+                                    int32_t vocab, int32_t k, const float* top_lse,
+                                    const float* lse, const float* dloss, float temperature,
+                                    void* dlogits, int32_t dlogits_dtype, int64_t ld_dlogits,
+                                    kronq_stream_t stream) {
+  if (vocab <= 0 || n_tok < 0 || k < 0)
+    return fail(KRONQ_ERR_SHAPE, "vocab must be positive, n_tok and k >= 0");
+  if (n_tok == 0) return KRONQ_OK;
+  if (!lse || !dloss || !dlogits)
+    return fail(KRONQ_ERR_INVALID_ARG, "lse, dloss and dlogits are required");
+  KQ_TRY(check_distill(logits, logits_dtype, ld_logits, ids, ld_ids, top, top_dtype, ld_top, n_tok,
+                       vocab, k, temperature, dlogits, dlogits_dtype, ld_dlogits));
+  KQ_TRY(kronq_device_check());
+  const DistillArgs a{logits, logits_dtype, ld_logits, ids, ld_ids, top, top_dtype, ld_top,
+                      n_tok, vocab, k, top_lse, dloss, temperature, lse, nullptr, nullptr,
+                      dlogits, dlogits_dtype, ld_dlogits};
+  return run_distill(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 // ----------------------------------------------------------------------------- allocation

@@ -98,6 +98,72 @@ kronq_status run_pack_grid(const float* scale, const float* zero, int d_out, int
 size_t qlinear_workspace_bytes(int d_out, int d_in, int n_tok);
 kronq_status run_qlinear(const QlinearArgs& q, void* ws, cudaStream_t stream);
 
+// i8matmul.cu: y = s_t s_o (q c^T - z_o sum_t), exact int32 sums (d_in <= kMaxI8Width).
+struct I8MatmulArgs {
+  const int8_t* q;         // n x d_in, stride ld_q (a multiple of 16, 16-byte aligned base)
+  int64_t ld_q;
+  const float* tok_scale;
+  const int32_t* tok_sum;  // may be NULL when zero is NULL
+  int n;
+  const void* codes;       // d_out x d_in, stride ld_codes (as ld_q)
+  int64_t ld_codes;
+  int is_signed;           // int8 codes (else uint8)
+  const float* scale;
+  const float* zero;       // may be NULL
+  const float* out_div;    // may be NULL: channel scales are divided by it
+  int d_out, d_in;
+  void* y;
+  int y_dtype;
+  int64_t ld_y;
+};
+constexpr int kMaxI8Width = 65536;     // 128 * 255 * 65536 < 2^31
+kronq_status run_i8matmul(const I8MatmulArgs& a, cudaStream_t stream);
+
+// tokquant.cu: per-token 8-bit activations (with the input transforms) and the output transforms.
+struct QuantTokensArgs {
+  const void* x;
+  int x_dtype;
+  int64_t ld_x;
+  int n, d;
+  const float* s_x;        // NULL: no scaling
+  const int8_t* sign_in;   // NULL: no rotation
+  int8_t* q;
+  int64_t ld_q;
+  float* tok_scale;
+  int32_t* tok_sum;
+};
+constexpr int kMaxRotatedWidth = 53248;  // a rotated token is held in shared memory (fp32)
+kronq_status run_quant_tokens(const QuantTokensArgs& q, cudaStream_t stream);
+// y = S_G^-1 U^T yp for n <= 65535 tokens (s_g NULL: no scaling)
+kronq_status run_out_transform(const float* yp, int64_t ld_yp, int n, int d, const float* s_g,
+                               const int8_t* sign_out, void* y, int y_dtype, int64_t ld_y,
+                               cudaStream_t stream);
+
+// distill.cu: distillation from a teacher's top logits. lse_in NULL: the loss (and lse, and the
+// gradient when dlogits is given); lse_in given: the gradient alone.
+struct DistillArgs {
+  const void* logits;
+  int logits_dtype;
+  int64_t ld_logits;
+  const int32_t* ids;
+  int64_t ld_ids;
+  const void* top;
+  int top_dtype;
+  int64_t ld_top;
+  int n, v, k;
+  const float* top_lse;
+  const float* row_weight;
+  float temperature;
+  const float* lse_in;
+  float* loss;
+  float* lse;
+  void* dlogits;
+  int dlogits_dtype;
+  int64_t ld_dlogits;
+};
+constexpr int kMaxDistillTop = 1024;
+kronq_status run_distill(const DistillArgs& q, cudaStream_t stream);
+
 // Zero structure of GEMM operands (the zeros must be stored), used to skip K ranges:
 //   GEMM_A_UPPER  A[m][k] = 0 for k < m
 //   GEMM_B_UPPER  op(B)[k][n] = 0 for k > n

@@ -27,6 +27,8 @@ ERR_TIMEOUT = 7
 
 DTYPE_BF16 = 0
 DTYPE_F32 = 1
+DTYPE_U8 = 2
+DTYPE_S8 = 3
 
 BIIP_SCALE_IN = 1
 BIIP_SCALE_OUT = 2
@@ -51,6 +53,8 @@ SYMBOLS = (
     "kronq_quantize_layer_twosided_workspace_size", "kronq_quantize_layer_twosided",
     "kronq_packed_codes_bytes", "kronq_pack_codes", "kronq_packed_grid_bytes", "kronq_pack_grid",
     "kronq_qlinear_workspace_size", "kronq_qlinear",
+    "kronq_quantize_tokens", "kronq_matmul_i8", "kronq_qlinear8_workspace_size", "kronq_qlinear8",
+    "kronq_distill", "kronq_distill_backward",
 )
 
 
@@ -126,6 +130,21 @@ def load_library(path: str = LIB_PATH):
         "kronq_qlinear": (c_i32, [c_void_p, c_i32, c_i64, c_i32, c_void_p, c_void_p,
                                   c_i32, c_void_p, c_void_p, c_void_p, c_void_p, c_u32, c_i32,
                                   c_i32, c_i32, c_void_p, c_i64, c_void_p, c_sz, c_void_p]),
+        "kronq_quantize_tokens": (c_i32, [c_void_p, c_i32, c_i64, c_i32, c_i32, c_void_p, c_void_p,
+                                          c_u32, c_void_p, c_i64, c_void_p, c_void_p, c_void_p]),
+        "kronq_matmul_i8": (c_i32, [c_void_p, c_i64, c_void_p, c_void_p, c_i32, c_void_p, c_i32,
+                                    c_i64, c_void_p, c_void_p, c_i32, c_i32, c_void_p, c_i32,
+                                    c_i64, c_void_p]),
+        "kronq_qlinear8_workspace_size": (c_sz, [c_i32, c_i32, c_i32, c_u32]),
+        "kronq_qlinear8": (c_i32, [c_void_p, c_i32, c_i64, c_i32, c_void_p, c_i32, c_i64, c_void_p,
+                                   c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_u32, c_i32,
+                                   c_i32, c_void_p, c_i32, c_i64, c_void_p, c_sz, c_void_p]),
+        "kronq_distill": (c_i32, [c_void_p, c_i32, c_i64, c_void_p, c_i64, c_void_p, c_i32, c_i64,
+                                  c_i32, c_i32, c_i32, c_void_p, c_void_p, c_flt, c_void_p,
+                                  c_void_p, c_void_p, c_i32, c_i64, c_void_p]),
+        "kronq_distill_backward": (c_i32, [c_void_p, c_i32, c_i64, c_void_p, c_i64, c_void_p,
+                                           c_i32, c_i64, c_i32, c_i32, c_i32, c_void_p, c_void_p,
+                                           c_void_p, c_flt, c_void_p, c_i32, c_i64, c_void_p]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -170,6 +189,43 @@ def _rowstride(t):
     if t.dim() != 2 or t.stride(1) != 1:
         raise ValueError("expected a 2-D tensor with unit column stride")
     return t.stride(0)
+
+
+_FLOATS = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
+_BYTES = {torch.uint8: DTYPE_U8, torch.int8: DTYPE_S8}
+
+
+def _float_type(t, name):
+    if t.dtype not in _FLOATS:
+        raise ValueError(f"{name} must be bf16 or fp32")
+    return _FLOATS[t.dtype]
+
+
+def _want(name, t, dtype, *shape):
+    """A contiguous tensor of this type and shape, or None, which passes."""
+    if t is None:
+        return
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}")
+
+
+def _rows(name, t, rows, cols):
+    """The row stride of a rows x cols matrix with contiguous rows."""
+    if t.dim() != 2 or tuple(t.shape) != (rows, cols) or (cols > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be {rows} x {cols} with unit column stride")
+    if rows > 0x7fffffff or cols > 0x7fffffff:
+        raise ValueError(f"{name}: sizes must fit 32 bits")
+    return t.stride(0)
+
+
+def _on_one_device(stream, **tensors):
+    """All tensors on the current device: the library launches there."""
+    dev = torch.device("cuda", torch.cuda.current_device())
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the current device is {dev}")
+    if isinstance(stream, torch.cuda.Stream) and stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the current device is {dev}")
 
 
 # ------------------------------------------------------------------------------ status helpers
@@ -401,3 +457,123 @@ def kronq_qlinear(x, packed, packed_grid, s_x, s_g, sign_in, sign_out, flags, d_
                            int(d_out), d_in, int(bits), _p(y), _rowstride(y), _p(ws), wsb,
                            _stream(stream))
     _check(st, "kronq_qlinear")
+
+
+# ------------------------------------------------------------------------------ 7. 8-bit layer
+
+def kronq_quantize_tokens(x, q, tok_scale, tok_sum, s_x=None, sign_in=None, flags=0, stream=None):
+    """q (int8), tok_scale, tok_sum of x (n_tok x d_in, bf16 or fp32) after S_X^-1 and V (flags)."""
+    lib = load_library()
+    n_tok, d_in = x.shape
+    ld_x, ld_q = _rows("x", x, n_tok, d_in), _rows("q", q, n_tok, d_in)
+    if q.dtype != torch.int8:
+        raise ValueError("q must be int8")
+    _want("tok_scale", tok_scale, torch.float32, n_tok)
+    _want("tok_sum", tok_sum, torch.int32, n_tok)
+    _want("s_x", s_x, torch.float32, d_in)
+    _want("sign_in", sign_in, torch.int8, d_in)
+    xd = _float_type(x, "x")
+    _on_one_device(stream, x=x, q=q, tok_scale=tok_scale, tok_sum=tok_sum, s_x=s_x,
+                   sign_in=sign_in)
+    st = lib.kronq_quantize_tokens(_p(x), xd, ld_x, n_tok, d_in, _p(s_x), _p(sign_in), int(flags),
+                                   _p(q), ld_q, _p(tok_scale), _p(tok_sum), _stream(stream))
+    _check(st, "kronq_quantize_tokens")
+
+
+def _codes_args(codes, scale, zero):
+    d_out, d_in = codes.shape
+    if codes.dtype not in _BYTES:
+        raise ValueError("codes must be uint8 or int8")
+    _want("scale", scale, torch.float32, d_out)
+    _want("zero", zero, torch.float32, d_out)
+    return d_out, d_in, _BYTES[codes.dtype], _rows("codes", codes, d_out, d_in)
+
+
+def kronq_matmul_i8(q, tok_scale, tok_sum, codes, scale, zero, y, stream=None):
+    """y (n_tok x d_out, fp32 or bf16) = tok_scale scale (q codes^T - zero tok_sum)."""
+    lib = load_library()
+    d_out, d_in, cd, ld_codes = _codes_args(codes, scale, zero)
+    n_tok = q.shape[0]
+    ld_q, ld_y = _rows("q", q, n_tok, d_in), _rows("y", y, n_tok, d_out)
+    if q.dtype != torch.int8:
+        raise ValueError("q must be int8")
+    _want("tok_scale", tok_scale, torch.float32, n_tok)
+    _want("tok_sum", tok_sum, torch.int32, n_tok)
+    yd = _float_type(y, "y")
+    _on_one_device(stream, q=q, tok_scale=tok_scale, tok_sum=tok_sum, codes=codes, scale=scale,
+                   zero=zero, y=y)
+    st = lib.kronq_matmul_i8(_p(q), ld_q, _p(tok_scale), _p(tok_sum), n_tok, _p(codes), cd,
+                             ld_codes, _p(scale), _p(zero), d_out, d_in, _p(y), yd, ld_y,
+                             _stream(stream))
+    _check(st, "kronq_matmul_i8")
+
+
+def kronq_qlinear8_workspace_size(n_tok: int, d_out: int, d_in: int, flags: int) -> int:
+    return load_library().kronq_qlinear8_workspace_size(n_tok, d_out, d_in, int(flags))
+
+
+def kronq_qlinear8(x, codes, scale, zero, s_x, s_g, sign_in, sign_out, flags, y, workspace=None,
+                   stream=None):
+    """y (n_tok x d_out, fp32 or bf16) = S_G^-1 U^T W^' V S_X^-1 x in 8-bit integers."""
+    lib = load_library()
+    d_out, d_in, cd, ld_codes = _codes_args(codes, scale, zero)
+    n_tok = x.shape[0]
+    ld_x, ld_y = _rows("x", x, n_tok, d_in), _rows("y", y, n_tok, d_out)
+    for name, t, dtype, d in (("s_x", s_x, torch.float32, d_in), ("s_g", s_g, torch.float32, d_out),
+                              ("sign_in", sign_in, torch.int8, d_in),
+                              ("sign_out", sign_out, torch.int8, d_out)):
+        _want(name, t, dtype, d)
+    xd, yd = _float_type(x, "x"), _float_type(y, "y")
+    _on_one_device(stream, x=x, codes=codes, scale=scale, zero=zero, s_x=s_x, s_g=s_g,
+                   sign_in=sign_in, sign_out=sign_out, y=y, workspace=workspace)
+    ws, wsb = _workspace(lib.kronq_qlinear8_workspace_size(n_tok, d_out, d_in, int(flags)),
+                         x.device, workspace)
+    st = lib.kronq_qlinear8(_p(x), xd, ld_x, n_tok, _p(codes), cd, ld_codes, _p(scale), _p(zero),
+                            _p(s_x), _p(s_g), _p(sign_in), _p(sign_out), int(flags), d_out, d_in,
+                            _p(y), yd, ld_y, _p(ws), wsb, _stream(stream))
+    _check(st, "kronq_qlinear8")
+
+
+# ------------------------------------------------------------------------------ 8. distillation
+
+def _distill_args(logits, ids, top, dlogits):
+    n_tok, vocab = logits.shape
+    if ids.dim() != 2 or ids.dtype != torch.int32:
+        raise ValueError("ids must be a 2-D int32 tensor")
+    k = ids.shape[1]
+    head = (_p(logits), _float_type(logits, "logits"), _rows("logits", logits, n_tok, vocab),
+            _p(ids), _rows("ids", ids, n_tok, k), _p(top), _float_type(top, "top"),
+            _rows("top", top, n_tok, k), n_tok, vocab, k)
+    grad = (None, DTYPE_F32, 0) if dlogits is None else (
+        _p(dlogits), _float_type(dlogits, "dlogits"), _rows("dlogits", dlogits, n_tok, vocab))
+    return n_tok, head, grad
+
+
+def kronq_distill(logits, ids, top, loss, lse=None, dlogits=None, top_lse=None, row_weight=None,
+                  temperature=1.0, stream=None):
+    """loss (and lse) of student logits (n_tok x vocab) against the teacher's top logits `top` at
+    entries `ids` (n_tok x k); with dlogits also the gradient, in the same pass over the logits."""
+    lib = load_library()
+    n_tok, head, grad = _distill_args(logits, ids, top, dlogits)
+    for name, t in (("loss", loss), ("lse", lse), ("top_lse", top_lse),
+                    ("row_weight", row_weight)):
+        _want(name, t, torch.float32, n_tok)
+    _on_one_device(stream, logits=logits, ids=ids, top=top, loss=loss, lse=lse, dlogits=dlogits,
+                   top_lse=top_lse, row_weight=row_weight)
+    st = lib.kronq_distill(*head, _p(top_lse), _p(row_weight), float(temperature), _p(loss),
+                           _p(lse), *grad, _stream(stream))
+    _check(st, "kronq_distill")
+
+
+def kronq_distill_backward(logits, ids, top, lse, dloss, dlogits, top_lse=None, temperature=1.0,
+                           stream=None):
+    """dlogits from lse (of kronq_distill) and the upstream gradient dloss per token."""
+    lib = load_library()
+    n_tok, head, grad = _distill_args(logits, ids, top, dlogits)
+    for name, t in (("lse", lse), ("dloss", dloss), ("top_lse", top_lse)):
+        _want(name, t, torch.float32, n_tok)
+    _on_one_device(stream, logits=logits, ids=ids, top=top, lse=lse, dloss=dloss, dlogits=dlogits,
+                   top_lse=top_lse)
+    st = lib.kronq_distill_backward(*head, _p(top_lse), _p(lse), _p(dloss), float(temperature),
+                                    *grad, _stream(stream))
+    _check(st, "kronq_distill_backward")

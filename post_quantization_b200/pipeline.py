@@ -115,6 +115,55 @@ def quantize_sublayer(w, hx_sum, hg_sum, dxx_sum, inv_n, sign_in, sign_out, bits
     return r
 
 
+def byte_rows(codes):
+    """codes with a row stride of a multiple of 16 bytes and an aligned base (a copy only where the
+    rows are not laid out so already), as the 8-bit calls read them."""
+    rows, cols = codes.shape
+    ok = codes.data_ptr() % 16 == 0 and (rows == 1 or codes.stride(0) % 16 == 0)
+    if ok and (cols == 1 or codes.stride(1) == 1):
+        return codes
+    out = torch.zeros(rows, (cols + 15) // 16 * 16, dtype=codes.dtype, device=codes.device)
+    out = out[:, :cols]
+    out.copy_(codes)
+    return out
+
+
+class Linear8:
+    """A quantized layer run in 8-bit integers (kronq_qlinear8), for any number of tokens.
+
+    codes (uint8 or int8, 2..8 bits), scale and zero (one grid per row) come from the column solve;
+    a transform whose scale or signs are None is left out. The codes are laid out once. `ws`, a
+    Workspace, serves calls on one stream; calls on several streams need one each.
+    """
+
+    def __init__(self, codes, scale, zero, s_x=None, s_g=None, sign_in=None, sign_out=None):
+        if scale.dim() != 1:
+            raise ValueError("the 8-bit layer takes one grid per row (group 0)")
+        self.codes = byte_rows(codes)
+        self.scale, self.zero = scale, zero
+        self.s_x, self.s_g, self.sign_in, self.sign_out = s_x, s_g, sign_in, sign_out
+        self.flags = ((K.BIIP_SCALE_IN if s_x is not None else 0) |
+                      (K.BIIP_SCALE_OUT if s_g is not None else 0) |
+                      (K.BIIP_ROTATE_IN if sign_in is not None else 0) |
+                      (K.BIIP_ROTATE_OUT if sign_out is not None else 0))
+
+    @classmethod
+    def of(cls, r: SublayerResult, sign_in, sign_out):
+        """The layer of a solved sublayer (pipeline.quantize with group 0) under the full BiIP."""
+        return cls(r.codes, r.scale, r.zero, r.s_x, r.s_g, sign_in, sign_out)
+
+    def __call__(self, x, y=None, dtype=torch.bfloat16, ws=None, stream=None):
+        """x: n_tok x d_in (bf16 or fp32). Returns y (n_tok x d_out, `dtype` unless given)."""
+        d_out, d_in = self.codes.shape
+        if y is None:
+            y = torch.empty(x.shape[0], d_out, dtype=dtype, device=x.device)
+        wsz = K.kronq_qlinear8_workspace_size(x.shape[0], d_out, d_in, self.flags)
+        K.kronq_qlinear8(x, self.codes, self.scale, self.zero, self.s_x, self.s_g, self.sign_in,
+                         self.sign_out, self.flags, y,
+                         workspace=ws.get(wsz) if ws is not None else None, stream=stream)
+        return y
+
+
 def allocate_global(local_traces: dict, n_params: list, choices, avg_bits: float, device=None):
     """Bit widths of every sublayer of a stack whose sublayers are spread over ranks.
 
