@@ -484,7 +484,7 @@ KRONQ_API kronq_status kronq_qlinear8(const void* x, int32_t x_dtype, int64_t ld
  *            marks an absent entry, whose logit is not used; an id listed twice counts twice
  *   top      (device) n_tok x k teacher logits t, top_dtype BF16 or F32, row stride ld_top. -inf
  *            entries count nothing
- *   k        0 .. 1024; rows without any entry have loss 0 and gradient 0
+ *   k        0 .. 1024 (vocab up to 2^30); rows without any entry have loss 0 and gradient 0
  *   top_lse  (device, fp32, n_tok) or NULL; row_weight w (device, fp32, n_tok) or NULL (1). A row
  *            of weight 0 has loss 0 and gradient 0 whatever its logits hold
  *   temperature tau, in [1e-4, 1e4]

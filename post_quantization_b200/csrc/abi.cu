@@ -223,6 +223,7 @@ kronq_status check_distill(const void* logits, int32_t logits_dtype, int64_t ld_
                            float temperature, const void* dlogits, int32_t dlogits_dtype,
                            int64_t ld_dlogits) {
   KQ_TRY(check_float_matrix(logits, logits_dtype, ld_logits, n_tok, vocab, "logits"));
+  if (vocab > (1 << 30)) return fail(KRONQ_ERR_UNSUPPORTED, "vocab = %d exceeds 2^30", vocab);
   if (k > kMaxDistillTop)
     return fail(KRONQ_ERR_UNSUPPORTED, "k = %d exceeds %d listed entries", k, kMaxDistillTop);
   if (k > 0) {

@@ -9,6 +9,16 @@
 // The difference is taken before the scaling: it is exact or rounds relative to itself, nothing
 // overflows (a mask of the type's lowest value included), and the rounding of c moves an exponent
 // by 2^-24 of the difference only.
+//
+// A row is cut into cl slices of 16-byte vectors, one CTA each. Where the row's statistics are
+// needed the CTAs of a row form a cluster and exchange (m, s) through distributed shared memory.
+//   distill_hold_kernel     loss and gradient in one read: a thread keeps its vectors of z in
+//                           registers between the statistics and the gradient
+//   distill_stream_kernel   the loss alone, the gradient from a given lse, and loss + gradient of
+//                           rows too long to hold (which are then read twice)
+// Listed entries are few: their p, their part of the loss and their gradients are computed by
+// one thread each, which fetches its id, logit and z[id] while the row streams; the gradient of
+// a listed entry is stored over the streamed one after a barrier.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -20,9 +30,10 @@
 namespace kq {
 namespace {
 
-constexpr int DS_THREADS = 512;
-constexpr int DS_MAX_K = 1024;
-constexpr int DS_HASH = 2048;
+constexpr int DS_THREADS = 256;
+constexpr int DS_WARPS = DS_THREADS / 32;
+constexpr int DS_KPT_MAX = kMaxDistillTop / DS_THREADS;   // listed entries per thread
+constexpr int DS_MAX_CL = 8;                          // CTAs per row (portable cluster size)
 constexpr float kNegInf = -INFINITY;
 
 struct DsArgs {
@@ -41,6 +52,9 @@ struct DsArgs {
   void* dz;
   int64_t ld_dz;
   int v, k;
+  int64_t row0;            // the launch's first row
+  int cl;                  // CTAs per row
+  int hash_mask;           // entries of the id table in use - 1 (a power of two, >= 2 k)
   float tau;
   double inv_tau;
   float c;                 // log2(e) / tau
@@ -57,143 +71,464 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// streaming accesses: each byte is used once by this kernel
+__device__ __forceinline__ uint4 ds_ldg(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
+// ---- 16-byte vectors of z: VE elements, element 0 lowest
+template <typename T>
+struct Vec;
+template <>
+struct Vec<float> {
+  static constexpr int VE = 4;
+  static __device__ __forceinline__ void get(const uint4& r, float (&x)[4]) {
+    x[0] = __uint_as_float(r.x);
+    x[1] = __uint_as_float(r.y);
+    x[2] = __uint_as_float(r.z);
+    x[3] = __uint_as_float(r.w);
+  }
+  static __device__ __forceinline__ float max(const uint4& r) {
+    return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)),
+                 fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
+  }
+};
+template <>
+struct Vec<__nv_bfloat16> {
+  static constexpr int VE = 8;
+  static __device__ __forceinline__ void get(const uint4& r, float (&x)[8]) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ float max(const uint4& r) {
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&r);
+    const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+    return fmaxf(__low2float(m), __high2float(m));
+  }
+};
+
+// The part of a row that a CTA streams. Vector i covers elements [i VE - skew, i VE - skew + VE)
+// of the row, where skew is what the row starts past a 16-byte boundary; the row's first and last
+// vector may lie partly outside and are then read and written element by element.
+template <typename T>
+struct Slice {
+  const T* row;
+  int skew, v;
+  int i0, i1;              // this CTA's vectors
+  __device__ __forceinline__ Slice(const T* r, int v_, int part, int parts) : row(r), v(v_) {
+    skew = static_cast<int>((reinterpret_cast<uintptr_t>(r) & 15u) / sizeof(T));
+    const int nv = (v + skew + Vec<T>::VE - 1) / Vec<T>::VE;
+    const int per = (nv + parts - 1) / parts;
+    i0 = min(nv, part * per);
+    i1 = min(nv, i0 + per);
+  }
+  __device__ __forceinline__ int first(int i) const { return i * Vec<T>::VE - skew; }
+  __device__ __forceinline__ bool whole(int i) const {
+    return first(i) >= 0 && first(i) + Vec<T>::VE <= v;
+  }
+  // entry e is streamed by this CTA
+  __device__ __forceinline__ bool owns(int e) const {
+    const int i = (e + skew) / Vec<T>::VE;
+    return i >= i0 && i < i1;
+  }
+  // elements outside the row come as -inf
+  __device__ __forceinline__ uint4 load(int i) const {
+    if (whole(i)) return ds_ldg(row + first(i));
+    uint4 r;
+    uint32_t* w = reinterpret_cast<uint32_t*>(&r);
+#pragma unroll
+    for (int e = 0; e < Vec<T>::VE; ++e) {
+      const int j = first(i) + e;
+      const bool in = j >= 0 && j < v;
+      if constexpr (sizeof(T) == 4) {
+        w[e] = in ? reinterpret_cast<const uint32_t*>(row)[j] : 0xff800000u;
+      } else {
+        const uint32_t b = in ? reinterpret_cast<const uint16_t*>(row)[j] : 0xff80u;
+        w[e >> 1] = (e & 1) ? (w[e >> 1] | (b << 16)) : b;
+      }
+    }
+    return r;
+  }
+};
+
+// Stores of a vector's VE gradients: as 8- or 16-byte words where the gradient row is aligned the
+// way the logits' row is, else one by one.
+template <typename T, typename D>
+__device__ __forceinline__ void store_vec(const Slice<T>& s, D* dz, bool aligned, int i,
+                                          const float (&g)[Vec<T>::VE]) {
+  constexpr int VE = Vec<T>::VE;
+  const int j0 = s.first(i);
+  if (aligned && s.whole(i)) {
+    if constexpr (sizeof(D) == 4) {
+#pragma unroll
+      for (int e = 0; e < VE; e += 4)
+        __stcs(reinterpret_cast<float4*>(dz + j0 + e), make_float4(g[e], g[e + 1], g[e + 2],
+                                                                   g[e + 3]));
+    } else {
+      uint32_t w[VE / 2];
+#pragma unroll
+      for (int e = 0; e < VE / 2; ++e) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(g[2 * e], g[2 * e + 1]);
+        w[e] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      if constexpr (VE == 8)
+        __stcs(reinterpret_cast<uint4*>(dz + j0), make_uint4(w[0], w[1], w[2], w[3]));
+      else
+        __stcs(reinterpret_cast<uint2*>(dz + j0), make_uint2(w[0], w[1]));
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < VE; ++e)
+      if (j0 + e >= 0 && j0 + e < s.v) ds_st(dz + j0 + e, g[e]);
+  }
+}
+template <typename T, typename D>
+__device__ __forceinline__ bool store_aligned(const Slice<T>& s, const D* dz) {
+  constexpr int bytes = Vec<T>::VE * sizeof(D) < 16 ? Vec<T>::VE * sizeof(D) : 16;
+  return (reinterpret_cast<uintptr_t>(dz) + (bytes - s.skew * sizeof(D) % bytes)) % bytes == 0;
+}
+
 // Running maximum and sum of 2^((z - m) c). m = -inf, s = 0: nothing but -inf seen.
 struct RunSum {
   float m, s;
 };
 __device__ __forceinline__ RunSum ds_join(RunSum a, RunSum b, float c) {
-  if (b.m == kNegInf && b.s == 0.f) return a;
-  if (a.m == kNegInf && a.s == 0.f) return b;
   const float m = fmaxf(a.m, b.m);
-  return {m, a.s * ex2((a.m - m) * c) + b.s * ex2((b.m - m) * c)};
+  const float fa = a.m == m ? 1.f : ex2((a.m - m) * c);
+  const float fb = b.m == m ? 1.f : ex2((b.m - m) * c);
+  return {m, a.s * fa + b.s * fb};
+}
+template <int W>
+__device__ __forceinline__ RunSum ds_join_lanes(RunSum r, float c) {
+#pragma unroll
+  for (int o = W / 2; o; o >>= 1)
+    r = ds_join(r, {__shfl_xor_sync(0xffffffffu, r.m, o), __shfl_xor_sync(0xffffffffu, r.s, o)}, c);
+  return r;
+}
+// terms of one vector against the running maximum, which already covers it
+template <typename T>
+__device__ __forceinline__ float ds_terms(const uint4& raw, float m, float c) {
+  float x[Vec<T>::VE];
+  Vec<T>::get(raw, x);
+  float s = 0.f;
+#pragma unroll
+  for (int e = 0; e < Vec<T>::VE; ++e) s += ex2((x[e] - m) * c);
+  return s;
 }
 
-// The teacher's side of one row, in shared memory.
-struct Teacher {
-  int id[DS_MAX_K];        // entry, or -1 where absent
-  float p[DS_MAX_K];
-  float logp[DS_MAX_K];
-  int key[DS_HASH];        // backward: id -> first j that lists it
-  int first[DS_HASH];
-  float mass;
-  int repeated;            // some id is listed twice
+__device__ __forceinline__ void ds_cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void ds_cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ds_remote(const void* p, uint32_t rank) {
+  uint32_t a;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+
+struct DsShared {
+  RunSum row[DS_WARPS];          // statistics per warp
+  RunSum list[DS_WARPS];         // and of the listed logits
+  RunSum mine;                   // this CTA's statistics, read by the cluster
+  double loss[DS_WARPS];
+  float mass[DS_WARPS];
 };
 
-// p, log p and P of the row by warp 0. Entries whose id is outside 0 .. v - 1 are absent; their
-// logits are not looked at.
-__device__ __forceinline__ void ds_teacher(const DsArgs& a, int64_t row, Teacher& te) {
-  const int lane = threadIdx.x;
-  auto logit = [&](int j) {
-    const int64_t o = row * a.ld_top + j;
-    return a.top_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.top)[o])
-                      : static_cast<const float*>(a.top)[o];
-  };
-  const float it = static_cast<float>(a.inv_tau);
-  float m = kNegInf;
-  for (int j = lane; j < a.k; j += 32) {
-    const int id = a.ids[row * a.ld_ids + j];
-    const bool there = id >= 0 && id < a.v;
-    te.id[j] = there ? id : -1;
-    if (there) m = fmaxf(m, logit(j));
+// With a gradient, in dynamic shared memory: the list, for repeated ids, and a table from an id to
+// the first j that lists it and how many do.
+struct IdTable {
+  float* p;                      // k
+  int* id;                       // k
+  int* key;                      // hash_mask + 1 each
+  int* first;
+  int* count;
+  __device__ __forceinline__ explicit IdTable(const DsArgs& a) {
+    extern __shared__ int ds_table[];
+    key = ds_table;
+    first = key + a.hash_mask + 1;
+    count = first + a.hash_mask + 1;
+    id = count + a.hash_mask + 1;
+    p = reinterpret_cast<float*>(id + a.k);
   }
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (m == kNegInf) m = 0.f;                   // only -inf logits: every p below is 0
-  float s = 0.f;
-  for (int j = lane; j < a.k; j += 32)
-    if (te.id[j] >= 0) s += expf((logit(j) - m) * it);
-  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  // log p_j = t_j / tau - norm, in fp64: the difference of two numbers of the logits' size
-  const double norm = a.top_lse ? static_cast<double>(a.top_lse[row])
-                                : m * a.inv_tau + (s == 0.f ? 0.f : logf(s));
-  float mass = 0.f;
-  for (int j = lane; j < a.k; j += 32) {
-    const float lp =
-        te.id[j] >= 0 ? static_cast<float>(logit(j) * a.inv_tau - norm) : kNegInf;
-    te.logp[j] = lp;
-    te.p[j] = expf(lp);
-    mass += te.p[j];
-  }
-  for (int o = 16; o; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
-  if (lane == 0) te.mass = mass;
+};
+size_t id_table_bytes(const DsArgs& a) {
+  return (3 * (static_cast<size_t>(a.hash_mask) + 1) + 2 * static_cast<size_t>(a.k)) * 4;
 }
 
-// Which j is the first to list its id (open addressing; called by the whole CTA).
-__device__ __forceinline__ void ds_hash(const DsArgs& a, Teacher& te) {
-  for (int i = threadIdx.x; i < DS_HASH; i += blockDim.x) {
-    te.key[i] = -1;
-    te.first[i] = DS_MAX_K;
-  }
-  if (threadIdx.x == 0) te.repeated = 0;
-  __syncthreads();
-  for (int j = threadIdx.x; j < a.k; j += blockDim.x) {
-    const int id = te.id[j];
-    if (id < 0) continue;
-    uint32_t h = (static_cast<uint32_t>(id) * 2654435761u) >> 21;     // 11 bits
-    while (true) {
-      const int old = atomicCAS(&te.key[h], -1, id);
-      if (old == -1 || old == id) break;
-      h = (h + 1) & (DS_HASH - 1);
+// The listed entries of a row: thread t has entries t, t + 256, ... (KPT of them)
+template <int KPT>
+struct Entries {
+  int id[KPT];                   // -1: absent
+  float t[KPT], z[KPT], p[KPT];
+};
+
+__device__ __forceinline__ uint32_t ds_slot(const DsArgs& a, int id) {
+  return (static_cast<uint32_t>(id) * 2654435761u >> 16) & a.hash_mask;
+}
+
+// z[id] is read where it is used: for the loss (all entries), and for the gradients of the entries
+// in the CTA's own slice (other slices may already be overwritten when dz is z).
+template <typename T, int KPT>
+__device__ __forceinline__ void load_entries(const DsArgs& a, int64_t row, const Slice<T>& s,
+                                             bool all, Entries<KPT>& e) {
+#pragma unroll
+  for (int i = 0; i < KPT; ++i) {
+    const int j = threadIdx.x + i * DS_THREADS;
+    e.id[i] = -1;
+    e.t[i] = kNegInf;
+    e.z[i] = 0.f;
+    if (j < a.k) {
+      const int id = a.ids[row * a.ld_ids + j];
+      if (id >= 0 && id < a.v) {
+        const int64_t o = row * a.ld_top + j;
+        e.id[i] = id;
+        e.t[i] = a.top_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.top)[o])
+                            : static_cast<const float*>(a.top)[o];
+        if (all || s.owns(id)) e.z[i] = ds_ld(s.row + id);
+      }
     }
-    atomicMin(&te.first[h], j);
   }
-  __syncthreads();
-}
-__device__ __forceinline__ int ds_first(const Teacher& te, int id) {
-  uint32_t h = (static_cast<uint32_t>(id) * 2654435761u) >> 21;
-  while (te.key[h] != id) h = (h + 1) & (DS_HASH - 1);
-  return te.first[h];
 }
 
-// One CTA per row. LSE: the row's log-sum-exp is computed (else lse_in); GRAD: dz is written.
-template <typename T, typename D, bool LSE, bool GRAD>
-__global__ void __launch_bounds__(DS_THREADS) distill_kernel(DsArgs a) {
-  __shared__ Teacher te;
-  __shared__ RunSum red[DS_THREADS / 32];
-  __shared__ double red_loss[DS_THREADS / 32];
-  const int64_t row = blockIdx.x;
+// Joins the CTA's (and, with a cluster, the row's) statistics and the listed entries'; gives p and,
+// in the CTA that reports the row, the loss. GRAD: fills the id table.
+template <bool LSE, bool GRAD, int KPT>
+__device__ __forceinline__ void row_statistics(const DsArgs& a, int64_t row, int part, float w,
+                                               DsShared& sh, RunSum& rs, Entries<KPT>& e,
+                                               float& mass) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  RunSum ls{kNegInf, 0.f};
+#pragma unroll
+  for (int i = 0; i < KPT; ++i)
+    if (e.t[i] != kNegInf) ls = ds_join(ls, {e.t[i], 1.f}, a.c);   // a NaN logit makes s NaN
+  ls = ds_join_lanes<32>(ls, a.c);
+  if (LSE) rs = ds_join_lanes<32>(rs, a.c);
+  if (lane == 0) {
+    sh.list[warp] = ls;
+    if (LSE) sh.row[warp] = rs;
+  }
+  __syncthreads();
+  ls = ds_join_lanes<DS_WARPS>(sh.list[lane % DS_WARPS], a.c);
+  if (LSE) {
+    rs = ds_join_lanes<DS_WARPS>(sh.row[lane % DS_WARPS], a.c);
+    if (a.cl > 1) {
+      if (tid == 0) sh.mine = rs;
+      ds_cluster_arrive();
+      ds_cluster_wait();
+      RunSum r{kNegInf, 0.f};
+      if (lane < a.cl) r = {ds_remote(&sh.mine.m, lane), ds_remote(&sh.mine.s, lane)};
+      rs = ds_join_lanes<DS_MAX_CL>(r, a.c);       // lanes 0 .. 7 hold the row's
+      rs = {__shfl_sync(0xffffffffu, rs.m, 0), __shfl_sync(0xffffffffu, rs.s, 0)};
+      ds_cluster_arrive();                         // waited for before the CTA ends
+    }
+  }
+  // log p_j = t_j / tau - L_t in fp64: the difference of two numbers of the logits' size
+  const double norm = a.top_lse ? static_cast<double>(a.top_lse[row])
+                                : ls.m * a.inv_tau + logf(ls.s);
+  const double lse = LSE ? rs.m * a.inv_tau + logf(rs.s) : 0.0;   // -inf where nothing was seen
+  double part_loss = 0.0;
+  mass = 0.f;
+#pragma unroll
+  for (int i = 0; i < KPT; ++i) {
+    const int j = tid + i * DS_THREADS;
+    e.p[i] = 0.f;
+    if (j >= a.k) break;
+    if (e.t[i] != kNegInf) {
+      const double lp = e.t[i] * a.inv_tau - norm;
+      const float p = expf(static_cast<float>(lp));
+      e.p[i] = p;
+      mass += p;
+      // a listed entry that the student masks has an infinite loss
+      if (LSE && p != 0.f)
+        part_loss += e.z[i] == kNegInf ? static_cast<double>(INFINITY)
+                                       : p * (lp - e.z[i] * a.inv_tau + lse);
+    }
+    if (GRAD) {
+      const IdTable table(a);
+      table.p[j] = e.p[i];
+      table.id[j] = e.id[i];
+      if (e.id[i] >= 0) {
+        uint32_t h = ds_slot(a, e.id[i]);
+        while (true) {                             // at most k of >= 2 k slots are taken
+          const int old = atomicCAS(&table.key[h], -1, e.id[i]);
+          if (old == -1 || old == e.id[i]) break;
+          h = (h + 1) & a.hash_mask;
+        }
+        atomicMin(&table.first[h], j);
+        atomicAdd(&table.count[h], 1);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    mass += __shfl_xor_sync(0xffffffffu, mass, o);
+    if (LSE) part_loss += __shfl_xor_sync(0xffffffffu, part_loss, o);
+  }
+  if (lane == 0) {
+    sh.mass[warp] = mass;
+    if (LSE) sh.loss[warp] = part_loss;
+  }
+  __syncthreads();
+  mass = 0.f;
+#pragma unroll
+  for (int i = 0; i < DS_WARPS; ++i) mass += sh.mass[i];
+  if (LSE && tid == 0 && part == 0) {
+    double tot = 0.0;
+    for (int i = 0; i < DS_WARPS; ++i) tot += sh.loss[i];
+    a.loss[row] = w == 0.f ? 0.f : static_cast<float>(static_cast<double>(w) * a.tau * a.tau * tot);
+    if (a.lse) a.lse[row] = static_cast<float>(lse);
+  }
+}
+
+__device__ __forceinline__ void clear_table(const DsArgs& a) {
+  const IdTable table(a);
+  for (int i = threadIdx.x; i <= a.hash_mask; i += DS_THREADS) {
+    table.key[i] = -1;
+    table.first[i] = kMaxDistillTop;
+    table.count[i] = 0;
+  }
+}
+
+// Gradients of the listed entries in this CTA's slice: the first thread that lists an id adds up
+// all its p, in the order of the list. patch_id = -1: not this thread's to store.
+template <typename T, int KPT>
+__device__ __forceinline__ void list_gradients(const DsArgs& a, const Slice<T>& s,
+                                               const Entries<KPT>& e, RunSum rs, float coef,
+                                               float wt, float (&patch)[KPT],
+                                               int (&patch_id)[KPT]) {
+  const IdTable table(a);
+#pragma unroll
+  for (int i = 0; i < KPT; ++i) {
+    const int j = threadIdx.x + i * DS_THREADS;
+    patch_id[i] = -1;
+    patch[i] = 0.f;
+    if (j < a.k && e.id[i] >= 0 && s.owns(e.id[i])) {
+      uint32_t h = ds_slot(a, e.id[i]);
+      while (table.key[h] != e.id[i]) h = (h + 1) & a.hash_mask;
+      if (table.first[h] == j) {
+        float p = e.p[i];
+        if (table.count[h] > 1)
+          for (int l = j + 1; l < a.k; ++l)
+            if (table.id[l] == e.id[i]) p += table.p[l];
+        patch_id[i] = e.id[i];
+        if (wt != 0.f)
+          patch[i] = coef == 0.f ? -wt * p : fmaf(coef, ex2((e.z[i] - rs.m) * a.c), -wt * p);
+      }
+    }
+  }
+}
+
+template <typename T, typename D>
+__device__ __forceinline__ void put_gradients(const Slice<T>& s, D* dz, bool aligned, int i,
+                                              const uint4& raw, float m, float c, float coef) {
+  float x[Vec<T>::VE], g[Vec<T>::VE];
+  Vec<T>::get(raw, x);
+#pragma unroll
+  for (int e = 0; e < Vec<T>::VE; ++e) g[e] = coef == 0.f ? 0.f : coef * ex2((x[e] - m) * c);
+  store_vec<T, D>(s, dz, aligned, i, g);
+}
+
+// w tau P / s: no gradient where the weight or the teacher's list is empty, none by q where z
+// holds nothing but -inf
+__device__ __forceinline__ float ds_coef(float wt, float mass, float s) {
+  return (wt == 0.f || mass == 0.f || s == 0.f) ? 0.f : wt * mass / s;
+}
+
+// Loss and gradient; NV vectors of z per thread stay in registers.
+template <typename T, typename D, int NV, int KPT>
+__global__ void __launch_bounds__(DS_THREADS, NV > 8 ? 2 : (KPT == 1 ? 4 : 3)) distill_hold_kernel(DsArgs a) {
+  __shared__ DsShared sh;
+  const int64_t row = a.row0 + blockIdx.x / a.cl;
+  const int part = blockIdx.x % a.cl;
+  const int tid = threadIdx.x;
   const T* z = static_cast<const T*>(a.z) + row * a.ld_z;
+  const Slice<T> s(z, a.v, part, a.cl);
+  uint4 raw[NV];
+#pragma unroll
+  for (int n = 0; n < NV; ++n) {
+    const int i = s.i0 + tid + n * DS_THREADS;
+    if (i < s.i1) raw[n] = s.load(i);
+  }
+  Entries<KPT> e;
+  load_entries(a, row, s, part == 0, e);
+  clear_table(a);
   const float w = a.weight ? a.weight[row] : 1.f;
-  if (warp == 0) ds_teacher(a, row, te);
+  RunSum rs{kNegInf, 0.f};
+#pragma unroll
+  for (int n = 0; n < NV; ++n)
+    if (s.i0 + tid + n * DS_THREADS < s.i1) rs.m = fmaxf(rs.m, Vec<T>::max(raw[n]));
+  // a thread whose entries are all -inf has nothing to add (and no finite reference); NaN it has
+  const float m = rs.m == kNegInf ? 0.f : rs.m;
+#pragma unroll
+  for (int n = 0; n < NV; ++n)
+    if (s.i0 + tid + n * DS_THREADS < s.i1) rs.s += ds_terms<T>(raw[n], m, a.c);
+  float mass;
+  row_statistics<true, true, KPT>(a, row, part, w, sh, rs, e, mass);
+  const float wt = w * a.tau;
+  const float coef = ds_coef(wt, mass, rs.s);
+  float patch[KPT];
+  int patch_id[KPT];
+  list_gradients(a, s, e, rs, coef, wt, patch, patch_id);
+  D* dz = static_cast<D*>(a.dz) + row * a.ld_dz;
+  const bool al = store_aligned(s, dz);
+#pragma unroll
+  for (int n = 0; n < NV; ++n) {
+    const int i = s.i0 + tid + n * DS_THREADS;
+    if (i < s.i1) put_gradients<T, D>(s, dz, al, i, raw[n], rs.m, a.c, coef);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < KPT; ++i)
+    if (patch_id[i] >= 0) ds_st(dz + patch_id[i], patch[i]);
+  if (a.cl > 1) ds_cluster_wait();
+}
+
+// LSE: the row's statistics are taken from z (else lse_in). GRAD: dz is written.
+template <typename T, typename D, bool LSE, bool GRAD, int KPT>
+__global__ void __launch_bounds__(DS_THREADS) distill_stream_kernel(DsArgs a) {
+  __shared__ DsShared sh;
+  const int64_t row = a.row0 + blockIdx.x / a.cl;
+  const int part = blockIdx.x % a.cl;
+  const int tid = threadIdx.x;
+  const T* z = static_cast<const T*>(a.z) + row * a.ld_z;
+  const Slice<T> s(z, a.v, part, a.cl);
+  Entries<KPT> e;
+  load_entries(a, row, s, LSE && part == 0, e);
+  if (GRAD) clear_table(a);
+  const float w = a.weight ? a.weight[row] : 1.f;
+  constexpr int U = 4;                               // vectors in flight per thread
   RunSum rs{kNegInf, 0.f};
   if (LSE) {
-    for (int v = tid; v < a.v; v += DS_THREADS) {
-      const float x = ds_ld(z + v);
-      if (x > rs.m) {
-        rs.s *= ex2((rs.m - x) * a.c);
-        rs.m = x;
+    for (int i = s.i0 + tid; i < s.i1; i += U * DS_THREADS) {
+      uint4 raw[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i + u * DS_THREADS < s.i1) raw[u] = s.load(i + u * DS_THREADS);
+      float m = rs.m;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i + u * DS_THREADS < s.i1) m = fmaxf(m, Vec<T>::max(raw[u]));
+      if (m != rs.m) {
+        rs.s *= ex2((rs.m - m) * a.c);
+        rs.m = m;
       }
-      if (x != kNegInf) rs.s += ex2((x - rs.m) * a.c);
-    }
-    for (int o = 16; o; o >>= 1)
-      rs = ds_join(rs, {__shfl_xor_sync(0xffffffffu, rs.m, o),
-                        __shfl_xor_sync(0xffffffffu, rs.s, o)}, a.c);
-    if (lane == 0) red[warp] = rs;
-  }
-  __syncthreads();
-  if (LSE) {
-    rs = red[0];
-    for (int i = 1; i < DS_THREADS / 32; ++i) rs = ds_join(rs, red[i], a.c);
-    const double lse = rs.m * a.inv_tau + logf(rs.s);      // -inf where nothing was seen
-    double part = 0.0;
-    for (int j = tid; j < a.k; j += DS_THREADS) {
-      const float p = te.p[j];
-      if (p != 0.f) {
-        const float x = ds_ld(z + te.id[j]);
-        // a listed entry that the student masks has an infinite loss
-        part += x == kNegInf ? static_cast<double>(INFINITY)
-                             : p * (te.logp[j] - x * a.inv_tau + lse);
-      }
-    }
-    for (int o = 16; o; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
-    if (lane == 0) red_loss[warp] = part;
-    __syncthreads();
-    if (tid == 0) {
-      double tot = 0.0;
-      for (int i = 0; i < DS_THREADS / 32; ++i) tot += red_loss[i];
-      a.loss[row] = w == 0.f ? 0.f
-                             : static_cast<float>(static_cast<double>(w) * a.tau * a.tau * tot);
-      if (a.lse) a.lse[row] = static_cast<float>(lse);
+      if (m == kNegInf) m = 0.f;                     // nothing but -inf (or NaN) so far
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i + u * DS_THREADS < s.i1) rs.s += ds_terms<T>(raw[u], m, a.c);
     }
   } else {
     // q = 2^((z - m) c) / s with m = lse tau rounded to fp32, s = what the rounding left
@@ -201,46 +536,91 @@ __global__ void __launch_bounds__(DS_THREADS) distill_kernel(DsArgs a) {
     rs.m = l * a.tau;
     rs.s = l == kNegInf ? 0.f : expf(static_cast<float>(l - rs.m * a.inv_tau));
   }
-  if (!GRAD) return;
-  D* dz = static_cast<D*>(a.dz) + row * a.ld_dz;
-  const float wt = w * a.tau;
-  const float mass = te.mass;
-  // no gradient where the weight or the teacher's list is empty, none by q where z is all -inf
-  const float coef = (wt == 0.f || mass == 0.f || rs.s == 0.f) ? 0.f : wt * mass / rs.s;
-  ds_hash(a, te);
-  // the listed entries' gradients, read before the row is written (dz may be z)
-  float patch[DS_MAX_K / DS_THREADS];
-  int patch_id[DS_MAX_K / DS_THREADS];
+  float mass;
+  row_statistics<LSE, GRAD, KPT>(a, row, part, w, sh, rs, e, mass);
+  if (GRAD) {
+    const float wt = w * a.tau;
+    const float coef = ds_coef(wt, mass, rs.s);
+    float patch[KPT];
+    int patch_id[KPT];
+    list_gradients(a, s, e, rs, coef, wt, patch, patch_id);
+    D* dz = static_cast<D*>(a.dz) + row * a.ld_dz;
+    const bool al = store_aligned(s, dz);
+    // dz may be z: every entry's z[id] was read before the first barrier above
+    for (int i = s.i0 + tid; i < s.i1; i += U * DS_THREADS) {
+      uint4 raw[U];
 #pragma unroll
-  for (int i = 0; i < DS_MAX_K / DS_THREADS; ++i) {
-    const int j = tid + i * DS_THREADS;
-    patch_id[i] = -1;
-    if (j < a.k && te.id[j] >= 0 && ds_first(te, te.id[j]) == j) {
-      const int id = te.id[j];
-      float p = 0.f;
-      for (int l = j; l < a.k; ++l)
-        if (te.id[l] == id) p += te.p[l];
-      patch_id[i] = id;
-      patch[i] = coef == 0.f ? -wt * p
-                             : fmaf(coef, ex2((ds_ld(z + id) - rs.m) * a.c), -wt * p);
-      if (wt == 0.f) patch[i] = 0.f;
+      for (int u = 0; u < U; ++u)
+        if (i + u * DS_THREADS < s.i1) raw[u] = s.load(i + u * DS_THREADS);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i + u * DS_THREADS < s.i1)
+          put_gradients<T, D>(s, dz, al, i + u * DS_THREADS, raw[u], rs.m, a.c, coef);
     }
-  }
-  __syncthreads();
-  for (int v = tid; v < a.v; v += DS_THREADS)
-    ds_st(dz + v, coef == 0.f ? 0.f : coef * ex2((ds_ld(z + v) - rs.m) * a.c));
-  __syncthreads();
+    __syncthreads();
 #pragma unroll
-  for (int i = 0; i < DS_MAX_K / DS_THREADS; ++i)
-    if (patch_id[i] >= 0) ds_st(dz + patch_id[i], patch[i]);
+    for (int i = 0; i < KPT; ++i)
+      if (patch_id[i] >= 0) ds_st(dz + patch_id[i], patch[i]);
+  }
+  if (LSE && a.cl > 1) ds_cluster_wait();
+}
+
+kronq_status launch_rows(void (*kern)(DsArgs), DsArgs a, int n, bool cluster, bool table,
+                         const char* what, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(DS_THREADS);
+  cfg.dynamicSmemBytes = table ? id_table_bytes(a) : 0;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(a.cl);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster && a.cl > 1 ? 1 : 0;
+  const int most = 0x7fffffff / a.cl;              // rows per launch: grid x extents end there
+  for (a.row0 = 0; a.row0 < n; a.row0 += most) {
+    const int64_t rows = std::min<int64_t>(most, n - a.row0);
+    cfg.gridDim = dim3(static_cast<unsigned>(rows * a.cl));
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, a);
+    if (err != cudaSuccess) return fail(KRONQ_ERR_CUDA, "%s: %s", what, cudaGetErrorString(err));
+    KQ_TRY(check_launch(what));
+  }
+  return KRONQ_OK;
+}
+
+template <typename T, typename D, int KPT>
+kronq_status launch_distill(DsArgs a, int n, bool lse, bool grad, cudaStream_t stream) {
+  constexpr int NV = 8;
+  const int64_t vecs = (static_cast<int64_t>(a.v) + 2 * Vec<T>::VE - 2) / Vec<T>::VE;
+  if (!lse) {
+    // the gradient alone has no statistics to exchange: any number of slices, here of four
+    // vectors per thread
+    a.cl = static_cast<int>((vecs + 4 * DS_THREADS - 1) / (4 * DS_THREADS));
+    return launch_rows(distill_stream_kernel<T, D, false, true, KPT>, a, n, false, true,
+                       "distill_stream_kernel", stream);
+  }
+  // Slices: enough to give every SM two CTAs when rows are few, none shorter than one vector per
+  // thread.
+  a.cl = 1;
+  while (a.cl < DS_MAX_CL && static_cast<int64_t>(n) * a.cl < 2 * device_sms() &&
+         vecs > static_cast<int64_t>(a.cl) * DS_THREADS)
+    a.cl *= 2;
+  if (!grad)
+    return launch_rows(distill_stream_kernel<T, D, true, false, KPT>, a, n, true, false,
+                       "distill_stream_kernel", stream);
+  while (a.cl < DS_MAX_CL && vecs > static_cast<int64_t>(a.cl) * DS_THREADS * NV) a.cl *= 2;
+  const int64_t per = (vecs + a.cl - 1) / a.cl;
+  auto kern = per <= DS_THREADS * NV       ? distill_hold_kernel<T, D, NV, KPT>
+              : per <= DS_THREADS * 2 * NV ? distill_hold_kernel<T, D, 2 * NV, KPT>
+                                           : distill_stream_kernel<T, D, true, true, KPT>;
+  return launch_rows(kern, a, n, true, true, "distill kernel", stream);
 }
 
 template <typename T, typename D>
 kronq_status launch_distill(const DsArgs& a, int n, bool lse, bool grad, cudaStream_t stream) {
-  auto kern = lse ? (grad ? distill_kernel<T, D, true, true> : distill_kernel<T, D, true, false>)
-                  : distill_kernel<T, D, false, true>;
-  kern<<<n, DS_THREADS, 0, stream>>>(a);
-  return check_launch("distill_kernel");
+  return a.k <= DS_THREADS ? launch_distill<T, D, 1>(a, n, lse, grad, stream)
+                           : launch_distill<T, D, DS_KPT_MAX>(a, n, lse, grad, stream);
 }
 
 }  // namespace
@@ -263,6 +643,8 @@ kronq_status run_distill(const DistillArgs& q, cudaStream_t stream) {
   a.ld_dz = q.ld_dlogits;
   a.v = q.v;
   a.k = q.k;
+  a.hash_mask = 31;
+  while (a.hash_mask + 1 < 2 * a.k) a.hash_mask = 2 * a.hash_mask + 1;
   a.tau = q.temperature;
   a.inv_tau = 1.0 / static_cast<double>(q.temperature);
   a.c = static_cast<float>(1.4426950408889634 * a.inv_tau);
