@@ -5,10 +5,13 @@
 //     p_j  = exp(t_j / tau - L_t),   L_t = logsumexp_j(t_j / tau)  or the caller's top_lse
 //     loss = w tau^2 sum_j p_j (log p_j - z[id_j] / tau + lse),  lse = logsumexp_v(z_v / tau)
 //     dz_v = w tau (P q_v - sum_{j: id_j = v} p_j),  P = sum_j p_j,  q_v = exp(z_v / tau - lse)
-// z is streamed with a running maximum and sum per thread: sum of 2^((z - m) c), c = log2(e) / tau.
-// The difference is taken before the scaling: it is exact or rounds relative to itself, nothing
-// overflows (a mask of the type's lowest value included), and the rounding of c moves an exponent
-// by 2^-24 of the difference only.
+// z is streamed with a running maximum m and sum per thread: sum of 2^(z c - fl(m c)), with
+// c = log2(e) / tau. The exponent is one FMA, rounded relative to the small difference; the
+// rounding of m c is the same in a row's sum and in its q, where it cancels, and lse undoes it.
+// Where m c overflows (a row that holds nothing but the type's lowest value) the exponent is
+// (z - m) c instead.
+// Per element and use of z: an unpack, half a packed fp32 FMA, one ex2, half a packed fp32 add or
+// multiply. The two ex2 of loss + gradient (16 a cycle and SM) stay below the time of the bytes.
 //
 // A row is cut into cl slices of 16-byte vectors, one CTA each. Where the row's statistics are
 // needed the CTAs of a row form a cluster and exchange (m, s) through distributed shared memory.
@@ -58,6 +61,7 @@ struct DsArgs {
   float tau;
   double inv_tau;
   float c;                 // log2(e) / tau
+  double nat;              // inv_tau / c: from the exponents' unit to z / tau
 };
 
 __device__ __forceinline__ float ds_ld(const __nv_bfloat16* p) { return __bfloat162float(*p); }
@@ -81,17 +85,43 @@ __device__ __forceinline__ uint4 ds_ldg(const void* p) {
   return v;
 }
 
-// ---- 16-byte vectors of z: VE elements, element 0 lowest
+// ---- pairs of fp32 in one 64-bit register pair (packed arithmetic)
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// ---- 16-byte vectors of z: VE elements as VE / 2 pairs
 template <typename T>
 struct Vec;
 template <>
 struct Vec<float> {
   static constexpr int VE = 4;
-  static __device__ __forceinline__ void get(const uint4& r, float (&x)[4]) {
-    x[0] = __uint_as_float(r.x);
-    x[1] = __uint_as_float(r.y);
-    x[2] = __uint_as_float(r.z);
-    x[3] = __uint_as_float(r.w);
+  static constexpr uint32_t NONE = 0xff800000u;                 // -inf
+  static __device__ __forceinline__ void get(const uint4& r, uint64_t (&x)[2]) {
+    x[0] = pack2(__uint_as_float(r.x), __uint_as_float(r.y));
+    x[1] = pack2(__uint_as_float(r.z), __uint_as_float(r.w));
   }
   static __device__ __forceinline__ float max(const uint4& r) {
     return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)),
@@ -101,13 +131,12 @@ struct Vec<float> {
 template <>
 struct Vec<__nv_bfloat16> {
   static constexpr int VE = 8;
-  static __device__ __forceinline__ void get(const uint4& r, float (&x)[8]) {
+  static constexpr uint32_t NONE = 0xff80ff80u;
+  static __device__ __forceinline__ void get(const uint4& r, uint64_t (&x)[4]) {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i)
+      x[i] = pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
   }
   static __device__ __forceinline__ float max(const uint4& r) {
     const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&r);
@@ -115,114 +144,128 @@ struct Vec<__nv_bfloat16> {
     return fmaxf(__low2float(m), __high2float(m));
   }
 };
+template <typename T>
+__device__ __forceinline__ uint4 none_vec() {                   // a vector of -inf: adds nothing
+  return make_uint4(Vec<T>::NONE, Vec<T>::NONE, Vec<T>::NONE, Vec<T>::NONE);
+}
 
-// The part of a row that a CTA streams. Vector i covers elements [i VE - skew, i VE - skew + VE)
-// of the row, where skew is what the row starts past a 16-byte boundary; the row's first and last
-// vector may lie partly outside and are then read and written element by element.
+// The part of a row that a CTA streams: vectors [i0, i1) of the row's aligned 16-byte vectors. The
+// elements before the first and after the last vector (fewer than VE each) are part 0's, one
+// per thread.
 template <typename T>
 struct Slice {
   const T* row;
-  int skew, v;
-  int i0, i1;              // this CTA's vectors
+  int v, head, nvec;
+  int i0, i1;
+  int edge;                // this thread's edge element, or -1
   __device__ __forceinline__ Slice(const T* r, int v_, int part, int parts) : row(r), v(v_) {
-    skew = static_cast<int>((reinterpret_cast<uintptr_t>(r) & 15u) / sizeof(T));
-    const int nv = (v + skew + Vec<T>::VE - 1) / Vec<T>::VE;
-    const int per = (nv + parts - 1) / parts;
-    i0 = min(nv, part * per);
-    i1 = min(nv, i0 + per);
-  }
-  __device__ __forceinline__ int first(int i) const { return i * Vec<T>::VE - skew; }
-  __device__ __forceinline__ bool whole(int i) const {
-    return first(i) >= 0 && first(i) + Vec<T>::VE <= v;
+    constexpr int VE = Vec<T>::VE;
+    const int off = static_cast<int>((reinterpret_cast<uintptr_t>(r) & 15u) / sizeof(T));
+    head = min(v, off ? VE - off : 0);
+    nvec = (v - head) / VE;
+    const int per = (nvec + parts - 1) / parts;
+    i0 = min(nvec, part * per);
+    i1 = min(nvec, i0 + per);
+    const int t = threadIdx.x, tail0 = head + nvec * VE;
+    edge = -1;
+    if (part == 0) {
+      if (t < VE && t < head) edge = t;
+      if (t >= VE && t < 2 * VE && tail0 + t - VE < v) edge = tail0 + t - VE;
+    }
   }
   // entry e is streamed by this CTA
-  __device__ __forceinline__ bool owns(int e) const {
-    const int i = (e + skew) / Vec<T>::VE;
+  __device__ __forceinline__ bool owns(int e, int part) const {
+    if (e < head || e >= head + nvec * Vec<T>::VE) return part == 0;
+    const int i = (e - head) / Vec<T>::VE;
     return i >= i0 && i < i1;
   }
-  // elements outside the row come as -inf
   __device__ __forceinline__ uint4 load(int i) const {
-    if (whole(i)) return ds_ldg(row + first(i));
-    uint4 r;
-    uint32_t* w = reinterpret_cast<uint32_t*>(&r);
-#pragma unroll
-    for (int e = 0; e < Vec<T>::VE; ++e) {
-      const int j = first(i) + e;
-      const bool in = j >= 0 && j < v;
-      if constexpr (sizeof(T) == 4) {
-        w[e] = in ? reinterpret_cast<const uint32_t*>(row)[j] : 0xff800000u;
-      } else {
-        const uint32_t b = in ? reinterpret_cast<const uint16_t*>(row)[j] : 0xff80u;
-        w[e >> 1] = (e & 1) ? (w[e >> 1] | (b << 16)) : b;
-      }
-    }
-    return r;
+    return ds_ldg(row + head + static_cast<int64_t>(i) * Vec<T>::VE);
   }
 };
 
-// Stores of a vector's VE gradients: as 8- or 16-byte words where the gradient row is aligned the
-// way the logits' row is, else one by one.
-template <typename T, typename D>
-__device__ __forceinline__ void store_vec(const Slice<T>& s, D* dz, bool aligned, int i,
-                                          const float (&g)[Vec<T>::VE]) {
-  constexpr int VE = Vec<T>::VE;
-  const int j0 = s.first(i);
-  if (aligned && s.whole(i)) {
-    if constexpr (sizeof(D) == 4) {
+// Stores a vector's gradients at d: as 8- or 16-byte words where aligned, else one by one.
+template <typename D, int VE>
+__device__ __forceinline__ void store_vec(D* d, bool aligned, const uint64_t (&g)[VE / 2]) {
+  if constexpr (sizeof(D) == 4) {
+    if (aligned) {
 #pragma unroll
-      for (int e = 0; e < VE; e += 4)
-        __stcs(reinterpret_cast<float4*>(dz + j0 + e), make_float4(g[e], g[e + 1], g[e + 2],
-                                                                   g[e + 3]));
-    } else {
-      uint32_t w[VE / 2];
-#pragma unroll
-      for (int e = 0; e < VE / 2; ++e) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(g[2 * e], g[2 * e + 1]);
-        w[e] = *reinterpret_cast<const uint32_t*>(&h);
+      for (int e = 0; e < VE / 4; ++e) {
+        const float2 a = unpack2(g[2 * e]), b = unpack2(g[2 * e + 1]);
+        __stcs(reinterpret_cast<float4*>(d) + e, make_float4(a.x, a.y, b.x, b.y));
       }
-      if constexpr (VE == 8)
-        __stcs(reinterpret_cast<uint4*>(dz + j0), make_uint4(w[0], w[1], w[2], w[3]));
-      else
-        __stcs(reinterpret_cast<uint2*>(dz + j0), make_uint2(w[0], w[1]));
+      return;
     }
-  } else {
+  } else if (aligned) {
+    uint32_t w[VE / 2];
 #pragma unroll
-    for (int e = 0; e < VE; ++e)
-      if (j0 + e >= 0 && j0 + e < s.v) ds_st(dz + j0 + e, g[e]);
+    for (int e = 0; e < VE / 2; ++e) {
+      const __nv_bfloat162 h = __float22bfloat162_rn(unpack2(g[e]));
+      w[e] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    if constexpr (VE == 8)
+      __stcs(reinterpret_cast<uint4*>(d), make_uint4(w[0], w[1], w[2], w[3]));
+    else
+      __stcs(reinterpret_cast<uint2*>(d), make_uint2(w[0], w[1]));
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < VE / 2; ++e) {
+    const float2 a = unpack2(g[e]);
+    ds_st(d + 2 * e, a.x);
+    ds_st(d + 2 * e + 1, a.y);
   }
 }
 template <typename T, typename D>
 __device__ __forceinline__ bool store_aligned(const Slice<T>& s, const D* dz) {
   constexpr int bytes = Vec<T>::VE * sizeof(D) < 16 ? Vec<T>::VE * sizeof(D) : 16;
-  return (reinterpret_cast<uintptr_t>(dz) + (bytes - s.skew * sizeof(D) % bytes)) % bytes == 0;
+  return reinterpret_cast<uintptr_t>(dz + s.head) % bytes == 0;
 }
 
-// Running maximum and sum of 2^((z - m) c). m = -inf, s = 0: nothing but -inf seen.
+// Running maximum and sum of 2^(z c - fl(m c)). m = -inf, s = 0: nothing but -inf seen.
 struct RunSum {
   float m, s;
 };
-__device__ __forceinline__ RunSum ds_join(RunSum a, RunSum b, float c) {
-  const float m = fmaxf(a.m, b.m);
-  const float fa = a.m == m ? 1.f : ex2((a.m - m) * c);
-  const float fb = b.m == m ? 1.f : ex2((b.m - m) * c);
-  return {m, a.s * fa + b.s * fb};
+__device__ __forceinline__ bool ds_wide(float m, float c) { return !(fabsf(m * c) < INFINITY); }
+// the exponent of one element
+__device__ __forceinline__ float ds_exponent(float z, float m, float c) {
+  return ds_wide(m, c) ? (z - m) * c : fmaf(z, c, -(m * c));
 }
+__device__ __forceinline__ float ds_rescale(float from, float to, float c) {
+  return ex2(ds_wide(to, c) ? (from - to) * c : from * c - to * c);
+}
+// Joins groups of W consecutive lanes that hold the same W values in every group (W = 32: the
+// warp): the common maximum first, so that each lane rescales its sum once.
 template <int W>
 __device__ __forceinline__ RunSum ds_join_lanes(RunSum r, float c) {
+  float m;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(r.m));
+  float s = r.m == m ? r.s : r.s * ds_rescale(r.m, m, c);
 #pragma unroll
-  for (int o = W / 2; o; o >>= 1)
-    r = ds_join(r, {__shfl_xor_sync(0xffffffffu, r.m, o), __shfl_xor_sync(0xffffffffu, r.s, o)}, c);
-  return r;
+  for (int o = W / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return {m, s};
 }
-// terms of one vector against the running maximum, which already covers it
+// acc += the terms of one vector against a maximum that covers it
 template <typename T>
-__device__ __forceinline__ float ds_terms(const uint4& raw, float m, float c) {
-  float x[Vec<T>::VE];
+__device__ __forceinline__ uint64_t ds_terms(uint64_t acc, const uint4& raw, float m, float c) {
+  constexpr int NP = Vec<T>::VE / 2;
+  uint64_t x[NP];
   Vec<T>::get(raw, x);
-  float s = 0.f;
+  if (ds_wide(m, c)) {
 #pragma unroll
-  for (int e = 0; e < Vec<T>::VE; ++e) s += ex2((x[e] - m) * c);
-  return s;
+    for (int e = 0; e < NP; ++e) {
+      const float2 z = unpack2(x[e]);
+      acc = add2(acc, pack2(ex2((z.x - m) * c), ex2((z.y - m) * c)));
+    }
+  } else {
+    const uint64_t cc = pack2(c, c), ref = pack2(-(m * c), -(m * c));
+#pragma unroll
+    for (int e = 0; e < NP; ++e) {
+      const float2 d = unpack2(fma2(x[e], cc, ref));
+      acc = add2(acc, pack2(ex2(d.x), ex2(d.y)));
+    }
+  }
+  return acc;
 }
 
 __device__ __forceinline__ void ds_cluster_arrive() {
@@ -283,7 +326,7 @@ __device__ __forceinline__ uint32_t ds_slot(const DsArgs& a, int id) {
 // in the CTA's own slice (other slices may already be overwritten when dz is z).
 template <typename T, int KPT>
 __device__ __forceinline__ void load_entries(const DsArgs& a, int64_t row, const Slice<T>& s,
-                                             bool all, Entries<KPT>& e) {
+                                             int part, bool all, Entries<KPT>& e) {
 #pragma unroll
   for (int i = 0; i < KPT; ++i) {
     const int j = threadIdx.x + i * DS_THREADS;
@@ -297,10 +340,15 @@ __device__ __forceinline__ void load_entries(const DsArgs& a, int64_t row, const
         e.id[i] = id;
         e.t[i] = a.top_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.top)[o])
                             : static_cast<const float*>(a.top)[o];
-        if (all || s.owns(id)) e.z[i] = ds_ld(s.row + id);
+        if (all || s.owns(id, part)) e.z[i] = ds_ld(s.row + id);
       }
     }
   }
+}
+
+// -inf where nothing was seen
+__device__ __forceinline__ double ds_lse(const DsArgs& a, RunSum r) {
+  return (ds_wide(r.m, a.c) ? r.m * a.inv_tau : r.m * a.c * a.nat) + logf(r.s);
 }
 
 // Joins the CTA's (and, with a cluster, the row's) statistics and the listed entries'; gives p and,
@@ -310,82 +358,92 @@ __device__ __forceinline__ void row_statistics(const DsArgs& a, int64_t row, int
                                                DsShared& sh, RunSum& rs, Entries<KPT>& e,
                                                float& mass) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  RunSum ls{kNegInf, 0.f};
-#pragma unroll
-  for (int i = 0; i < KPT; ++i)
-    if (e.t[i] != kNegInf) ls = ds_join(ls, {e.t[i], 1.f}, a.c);   // a NaN logit makes s NaN
-  ls = ds_join_lanes<32>(ls, a.c);
-  if (LSE) rs = ds_join_lanes<32>(rs, a.c);
-  if (lane == 0) {
-    sh.list[warp] = ls;
-    if (LSE) sh.row[warp] = rs;
+  const bool lists = warp * 32 < a.k;            // some thread of the warp has an entry
+  if (LSE) {
+    rs = ds_join_lanes<32>(rs, a.c);
+    if (lane == 0) sh.row[warp] = rs;
   }
+  RunSum ls{kNegInf, 0.f};
+  if (lists) {
+#pragma unroll
+    for (int i = 0; i < KPT; ++i) ls.m = fmaxf(ls.m, e.t[i]);
+#pragma unroll
+    for (int i = 0; i < KPT; ++i)                // a NaN logit makes s NaN
+      if (e.t[i] != kNegInf) ls.s += ex2(ds_exponent(e.t[i], ls.m == kNegInf ? 0.f : ls.m, a.c));
+    ls = ds_join_lanes<32>(ls, a.c);
+  }
+  if (lane == 0) sh.list[warp] = ls;
   __syncthreads();
-  ls = ds_join_lanes<DS_WARPS>(sh.list[lane % DS_WARPS], a.c);
   if (LSE) {
     rs = ds_join_lanes<DS_WARPS>(sh.row[lane % DS_WARPS], a.c);
     if (a.cl > 1) {
       if (tid == 0) sh.mine = rs;
       ds_cluster_arrive();
       ds_cluster_wait();
-      RunSum r{kNegInf, 0.f};
-      if (lane < a.cl) r = {ds_remote(&sh.mine.m, lane), ds_remote(&sh.mine.s, lane)};
-      rs = ds_join_lanes<DS_MAX_CL>(r, a.c);       // lanes 0 .. 7 hold the row's
-      rs = {__shfl_sync(0xffffffffu, rs.m, 0), __shfl_sync(0xffffffffu, rs.s, 0)};
+      const int r = lane % DS_MAX_CL;
+      rs = {kNegInf, 0.f};
+      if (r < a.cl) rs = {ds_remote(&sh.mine.m, r), ds_remote(&sh.mine.s, r)};
+      rs = ds_join_lanes<DS_MAX_CL>(rs, a.c);
       ds_cluster_arrive();                         // waited for before the CTA ends
     }
   }
-  // log p_j = t_j / tau - L_t in fp64: the difference of two numbers of the logits' size
-  const double norm = a.top_lse ? static_cast<double>(a.top_lse[row])
-                                : ls.m * a.inv_tau + logf(ls.s);
-  const double lse = LSE ? rs.m * a.inv_tau + logf(rs.s) : 0.0;   // -inf where nothing was seen
   double part_loss = 0.0;
+  const bool report = LSE && part == 0;
+  const double lse = report ? ds_lse(a, rs) : 0.0;
   mass = 0.f;
 #pragma unroll
-  for (int i = 0; i < KPT; ++i) {
-    const int j = tid + i * DS_THREADS;
-    e.p[i] = 0.f;
-    if (j >= a.k) break;
-    if (e.t[i] != kNegInf) {
-      const double lp = e.t[i] * a.inv_tau - norm;
-      const float p = expf(static_cast<float>(lp));
-      e.p[i] = p;
-      mass += p;
-      // a listed entry that the student masks has an infinite loss
-      if (LSE && p != 0.f)
-        part_loss += e.z[i] == kNegInf ? static_cast<double>(INFINITY)
-                                       : p * (lp - e.z[i] * a.inv_tau + lse);
-    }
-    if (GRAD) {
-      const IdTable table(a);
-      table.p[j] = e.p[i];
-      table.id[j] = e.id[i];
-      if (e.id[i] >= 0) {
-        uint32_t h = ds_slot(a, e.id[i]);
-        while (true) {                             // at most k of >= 2 k slots are taken
-          const int old = atomicCAS(&table.key[h], -1, e.id[i]);
-          if (old == -1 || old == e.id[i]) break;
-          h = (h + 1) & a.hash_mask;
+  for (int i = 0; i < KPT; ++i) e.p[i] = 0.f;
+  if (lists) {
+    // log p_j = t_j / tau - L_t in fp64: the difference of two numbers of the logits' size
+    ls = ds_join_lanes<DS_WARPS>(sh.list[lane % DS_WARPS], a.c);
+    const double norm = a.top_lse ? static_cast<double>(a.top_lse[row]) : ds_lse(a, ls);
+#pragma unroll
+    for (int i = 0; i < KPT; ++i) {
+      const int j = tid + i * DS_THREADS;
+      if (j >= a.k) break;
+      if (e.t[i] != kNegInf) {
+        const double lp = e.t[i] * a.inv_tau - norm;
+        const float p = expf(static_cast<float>(lp));
+        e.p[i] = p;
+        mass += p;
+        // a listed entry that the student masks has an infinite loss
+        if (report && p != 0.f)
+          part_loss += e.z[i] == kNegInf ? static_cast<double>(INFINITY)
+                                         : p * (lp - e.z[i] * a.inv_tau + lse);
+      }
+      if (GRAD) {
+        const IdTable table(a);
+        table.p[j] = e.p[i];
+        table.id[j] = e.id[i];
+        if (e.id[i] >= 0) {
+          uint32_t h = ds_slot(a, e.id[i]);
+          while (true) {                           // at most k of >= 2 k slots are taken
+            const int old = atomicCAS(&table.key[h], -1, e.id[i]);
+            if (old == -1 || old == e.id[i]) break;
+            h = (h + 1) & a.hash_mask;
+          }
+          atomicMin(&table.first[h], j);
+          atomicAdd(&table.count[h], 1);
         }
-        atomicMin(&table.first[h], j);
-        atomicAdd(&table.count[h], 1);
       }
     }
-  }
+    __syncwarp();
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    mass += __shfl_xor_sync(0xffffffffu, mass, o);
-    if (LSE) part_loss += __shfl_xor_sync(0xffffffffu, part_loss, o);
+    for (int o = 16; o; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
+    if (report) {
+#pragma unroll
+      for (int o = 16; o; o >>= 1) part_loss += __shfl_xor_sync(0xffffffffu, part_loss, o);
+    }
   }
   if (lane == 0) {
     sh.mass[warp] = mass;
-    if (LSE) sh.loss[warp] = part_loss;
+    if (report) sh.loss[warp] = part_loss;
   }
   __syncthreads();
   mass = 0.f;
 #pragma unroll
   for (int i = 0; i < DS_WARPS; ++i) mass += sh.mass[i];
-  if (LSE && tid == 0 && part == 0) {
+  if (report && tid == 0) {
     double tot = 0.0;
     for (int i = 0; i < DS_WARPS; ++i) tot += sh.loss[i];
     a.loss[row] = w == 0.f ? 0.f : static_cast<float>(static_cast<double>(w) * a.tau * a.tau * tot);
@@ -407,7 +465,7 @@ __device__ __forceinline__ void clear_table(const DsArgs& a) {
 template <typename T, int KPT>
 __device__ __forceinline__ void list_gradients(const DsArgs& a, const Slice<T>& s,
                                                const Entries<KPT>& e, RunSum rs, float coef,
-                                               float wt, float (&patch)[KPT],
+                                               float wt, int part, float (&patch)[KPT],
                                                int (&patch_id)[KPT]) {
   const IdTable table(a);
 #pragma unroll
@@ -415,7 +473,7 @@ __device__ __forceinline__ void list_gradients(const DsArgs& a, const Slice<T>& 
     const int j = threadIdx.x + i * DS_THREADS;
     patch_id[i] = -1;
     patch[i] = 0.f;
-    if (j < a.k && e.id[i] >= 0 && s.owns(e.id[i])) {
+    if (j < a.k && e.id[i] >= 0 && s.owns(e.id[i], part)) {
       uint32_t h = ds_slot(a, e.id[i]);
       while (table.key[h] != e.id[i]) h = (h + 1) & a.hash_mask;
       if (table.first[h] == j) {
@@ -425,20 +483,41 @@ __device__ __forceinline__ void list_gradients(const DsArgs& a, const Slice<T>& 
             if (table.id[l] == e.id[i]) p += table.p[l];
         patch_id[i] = e.id[i];
         if (wt != 0.f)
-          patch[i] = coef == 0.f ? -wt * p : fmaf(coef, ex2((e.z[i] - rs.m) * a.c), -wt * p);
+          patch[i] = coef == 0.f ? -wt * p : fmaf(coef, ex2(ds_exponent(e.z[i], rs.m, a.c)), -wt * p);
       }
     }
   }
 }
 
 template <typename T, typename D>
-__device__ __forceinline__ void put_gradients(const Slice<T>& s, D* dz, bool aligned, int i,
-                                              const uint4& raw, float m, float c, float coef) {
-  float x[Vec<T>::VE], g[Vec<T>::VE];
+__device__ __forceinline__ void put_gradients(D* d, bool aligned, const uint4& raw, float m,
+                                              float c, float coef) {
+  constexpr int NP = Vec<T>::VE / 2;
+  uint64_t x[NP], g[NP];
   Vec<T>::get(raw, x);
+  if (coef == 0.f) {                                   // whatever z holds
 #pragma unroll
-  for (int e = 0; e < Vec<T>::VE; ++e) g[e] = coef == 0.f ? 0.f : coef * ex2((x[e] - m) * c);
-  store_vec<T, D>(s, dz, aligned, i, g);
+    for (int e = 0; e < NP; ++e) g[e] = 0;
+  } else if (ds_wide(m, c)) {
+#pragma unroll
+    for (int e = 0; e < NP; ++e) {
+      const float2 z = unpack2(x[e]);
+      g[e] = pack2(coef * ex2((z.x - m) * c), coef * ex2((z.y - m) * c));
+    }
+  } else {
+    const uint64_t cc = pack2(c, c), ref = pack2(-(m * c), -(m * c)), k = pack2(coef, coef);
+#pragma unroll
+    for (int e = 0; e < NP; ++e) {
+      const float2 t = unpack2(fma2(x[e], cc, ref));
+      g[e] = mul2(k, pack2(ex2(t.x), ex2(t.y)));
+    }
+  }
+  store_vec<D, Vec<T>::VE>(d, aligned, g);
+}
+template <typename T, typename D>
+__device__ __forceinline__ void put_edge(const Slice<T>& s, D* dz, float z, float m, float c,
+                                         float coef) {
+  if (s.edge >= 0) ds_st(dz + s.edge, coef == 0.f ? 0.f : coef * ex2(ds_exponent(z, m, c)));
 }
 
 // w tau P / s: no gradient where the weight or the teacher's list is empty, none by q where z
@@ -460,35 +539,46 @@ __global__ void __launch_bounds__(DS_THREADS, NV > 8 ? 2 : (KPT == 1 ? 4 : 3)) d
 #pragma unroll
   for (int n = 0; n < NV; ++n) {
     const int i = s.i0 + tid + n * DS_THREADS;
-    if (i < s.i1) raw[n] = s.load(i);
+    raw[n] = i < s.i1 ? s.load(i) : none_vec<T>();
   }
+  const float ze = s.edge >= 0 ? ds_ld(z + s.edge) : kNegInf;
   Entries<KPT> e;
-  load_entries(a, row, s, part == 0, e);
+  load_entries(a, row, s, part, part == 0, e);
   clear_table(a);
   const float w = a.weight ? a.weight[row] : 1.f;
-  RunSum rs{kNegInf, 0.f};
+  RunSum rs{ze, 0.f};
 #pragma unroll
-  for (int n = 0; n < NV; ++n)
-    if (s.i0 + tid + n * DS_THREADS < s.i1) rs.m = fmaxf(rs.m, Vec<T>::max(raw[n]));
-  // a thread whose entries are all -inf has nothing to add (and no finite reference); NaN it has
+  for (int n = 0; n < NV; ++n) rs.m = fmaxf(rs.m, Vec<T>::max(raw[n]));
+  // a thread whose entries are all -inf adds nothing, to any reference (NaN it adds)
   const float m = rs.m == kNegInf ? 0.f : rs.m;
+  uint64_t acc = pack2(ex2(ds_exponent(ze, m, a.c)), 0.f);
+#pragma unroll
+  for (int n = 0; n < NV; ++n) {
+    acc = ds_terms<T>(acc, raw[n], m, a.c);
+    asm volatile("" : "+l"(acc));                      // one vector unpacked at a time
+  }
+  rs.s = unpack2(acc).x + unpack2(acc).y;
+  // the gradient unpacks the vectors again: nothing unpacked lives across the statistics
 #pragma unroll
   for (int n = 0; n < NV; ++n)
-    if (s.i0 + tid + n * DS_THREADS < s.i1) rs.s += ds_terms<T>(raw[n], m, a.c);
+    asm volatile("" : "+r"(raw[n].x), "+r"(raw[n].y), "+r"(raw[n].z), "+r"(raw[n].w));
   float mass;
   row_statistics<true, true, KPT>(a, row, part, w, sh, rs, e, mass);
   const float wt = w * a.tau;
   const float coef = ds_coef(wt, mass, rs.s);
   float patch[KPT];
   int patch_id[KPT];
-  list_gradients(a, s, e, rs, coef, wt, patch, patch_id);
+  list_gradients(a, s, e, rs, coef, wt, part, patch, patch_id);
   D* dz = static_cast<D*>(a.dz) + row * a.ld_dz;
   const bool al = store_aligned(s, dz);
 #pragma unroll
   for (int n = 0; n < NV; ++n) {
     const int i = s.i0 + tid + n * DS_THREADS;
-    if (i < s.i1) put_gradients<T, D>(s, dz, al, i, raw[n], rs.m, a.c, coef);
+    if (i < s.i1)
+      put_gradients<T, D>(dz + s.head + static_cast<int64_t>(i) * Vec<T>::VE, al, raw[n], rs.m, a.c,
+                          coef);
   }
+  put_edge(s, dz, ze, rs.m, a.c, coef);
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < KPT; ++i)
@@ -506,35 +596,41 @@ __global__ void __launch_bounds__(DS_THREADS) distill_stream_kernel(DsArgs a) {
   const T* z = static_cast<const T*>(a.z) + row * a.ld_z;
   const Slice<T> s(z, a.v, part, a.cl);
   Entries<KPT> e;
-  load_entries(a, row, s, LSE && part == 0, e);
+  load_entries(a, row, s, part, LSE && part == 0, e);
   if (GRAD) clear_table(a);
   const float w = a.weight ? a.weight[row] : 1.f;
   constexpr int U = 4;                               // vectors in flight per thread
+  const float ze = s.edge >= 0 ? ds_ld(z + s.edge) : kNegInf;
   RunSum rs{kNegInf, 0.f};
   if (LSE) {
+    rs = {ze, ze == kNegInf ? 0.f : ex2(ds_exponent(ze, ze, a.c))};       // 1, or NaN
     for (int i = s.i0 + tid; i < s.i1; i += U * DS_THREADS) {
       uint4 raw[U];
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (i + u * DS_THREADS < s.i1) raw[u] = s.load(i + u * DS_THREADS);
+        raw[u] = i + u * DS_THREADS < s.i1 ? s.load(i + u * DS_THREADS) : none_vec<T>();
       float m = rs.m;
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (i + u * DS_THREADS < s.i1) m = fmaxf(m, Vec<T>::max(raw[u]));
-      if (m != rs.m) {
-        rs.s *= ex2((rs.m - m) * a.c);
+      for (int u = 0; u < U; ++u) m = fmaxf(m, Vec<T>::max(raw[u]));
+      if (m > rs.m) {
+        rs.s *= ds_rescale(rs.m, m, a.c);
         rs.m = m;
       }
-      if (m == kNegInf) m = 0.f;                     // nothing but -inf (or NaN) so far
+      if (!(m > kNegInf)) m = 0.f;                   // nothing but -inf (or NaN) so far
+      uint64_t acc = 0;
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (i + u * DS_THREADS < s.i1) rs.s += ds_terms<T>(raw[u], m, a.c);
+      for (int u = 0; u < U; ++u) acc = ds_terms<T>(acc, raw[u], m, a.c);
+      rs.s += unpack2(acc).x + unpack2(acc).y;
     }
   } else {
-    // q = 2^((z - m) c) / s with m = lse tau rounded to fp32, s = what the rounding left
+    // q = 2^(z c - fl(m c)) / s with m = lse tau rounded to fp32, s = what the roundings left
+    // (z tau^-1 - lse at z = lse tau, where q is not small)
     const float l = a.lse_in[row];
     rs.m = l * a.tau;
-    rs.s = l == kNegInf ? 0.f : expf(static_cast<float>(l - rs.m * a.inv_tau));
+    const double left = ds_wide(rs.m, a.c) ? l - rs.m * a.inv_tau
+                                           : (static_cast<double>(l) * a.tau * a.c -
+                                              static_cast<double>(rs.m * a.c)) * 0.69314718055994531;
+    rs.s = l == kNegInf ? 0.f : expf(static_cast<float>(left));
   }
   float mass;
   row_statistics<LSE, GRAD, KPT>(a, row, part, w, sh, rs, e, mass);
@@ -543,7 +639,7 @@ __global__ void __launch_bounds__(DS_THREADS) distill_stream_kernel(DsArgs a) {
     const float coef = ds_coef(wt, mass, rs.s);
     float patch[KPT];
     int patch_id[KPT];
-    list_gradients(a, s, e, rs, coef, wt, patch, patch_id);
+    list_gradients(a, s, e, rs, coef, wt, part, patch, patch_id);
     D* dz = static_cast<D*>(a.dz) + row * a.ld_dz;
     const bool al = store_aligned(s, dz);
     // dz may be z: every entry's z[id] was read before the first barrier above
@@ -555,8 +651,10 @@ __global__ void __launch_bounds__(DS_THREADS) distill_stream_kernel(DsArgs a) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (i + u * DS_THREADS < s.i1)
-          put_gradients<T, D>(s, dz, al, i + u * DS_THREADS, raw[u], rs.m, a.c, coef);
+          put_gradients<T, D>(dz + s.head + static_cast<int64_t>(i + u * DS_THREADS) * Vec<T>::VE,
+                              al, raw[u], rs.m, a.c, coef);
     }
+    put_edge(s, dz, ze, rs.m, a.c, coef);
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < KPT; ++i)
@@ -592,7 +690,7 @@ kronq_status launch_rows(void (*kern)(DsArgs), DsArgs a, int n, bool cluster, bo
 template <typename T, typename D, int KPT>
 kronq_status launch_distill(DsArgs a, int n, bool lse, bool grad, cudaStream_t stream) {
   constexpr int NV = 8;
-  const int64_t vecs = (static_cast<int64_t>(a.v) + 2 * Vec<T>::VE - 2) / Vec<T>::VE;
+  const int64_t vecs = static_cast<int64_t>(a.v) / Vec<T>::VE + 1;    // at most, and at least one
   if (!lse) {
     // the gradient alone has no statistics to exchange: any number of slices, here of four
     // vectors per thread
@@ -648,6 +746,7 @@ kronq_status run_distill(const DistillArgs& q, cudaStream_t stream) {
   a.tau = q.temperature;
   a.inv_tau = 1.0 / static_cast<double>(q.temperature);
   a.c = static_cast<float>(1.4426950408889634 * a.inv_tau);
+  a.nat = a.inv_tau / a.c;
   const bool lse = q.lse_in == nullptr, grad = q.dlogits != nullptr;
   const bool zb = q.logits_dtype == KRONQ_DTYPE_BF16, db = q.dlogits_dtype == KRONQ_DTYPE_BF16;
   if (zb) return db || !grad ? launch_distill<__nv_bfloat16, __nv_bfloat16>(a, q.n, lse, grad, stream)
