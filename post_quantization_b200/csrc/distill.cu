@@ -56,7 +56,8 @@ struct DsArgs {
   int64_t ld_dz;
   int v, k;
   int64_t row0;            // the launch's first row
-  int cl;                  // CTAs per row
+  int cl;                  // CTAs per row (the grid's x extent; y counts rows)
+  int per;                 // vectors per CTA
   int hash_mask;           // entries of the id table in use - 1 (a power of two, >= 2 k)
   float tau;
   double inv_tau;
@@ -158,12 +159,11 @@ struct Slice {
   int v, head, nvec;
   int i0, i1;
   int edge;                // this thread's edge element, or -1
-  __device__ __forceinline__ Slice(const T* r, int v_, int part, int parts) : row(r), v(v_) {
+  __device__ __forceinline__ Slice(const T* r, int v_, int part, int per) : row(r), v(v_) {
     constexpr int VE = Vec<T>::VE;
     const int off = static_cast<int>((reinterpret_cast<uintptr_t>(r) & 15u) / sizeof(T));
     head = min(v, off ? VE - off : 0);
     nvec = (v - head) / VE;
-    const int per = (nvec + parts - 1) / parts;
     i0 = min(nvec, part * per);
     i1 = min(nvec, i0 + per);
     const int t = threadIdx.x, tail0 = head + nvec * VE;
@@ -247,11 +247,12 @@ __device__ __forceinline__ RunSum ds_join_lanes(RunSum r, float c) {
 }
 // acc += the terms of one vector against a maximum that covers it
 template <typename T>
-__device__ __forceinline__ uint64_t ds_terms(uint64_t acc, const uint4& raw, float m, float c) {
+__device__ __forceinline__ uint64_t ds_terms(uint64_t acc, const uint4& raw, bool wide, float m,
+                                             float c) {
   constexpr int NP = Vec<T>::VE / 2;
   uint64_t x[NP];
   Vec<T>::get(raw, x);
-  if (ds_wide(m, c)) {
+  if (wide) {
 #pragma unroll
     for (int e = 0; e < NP; ++e) {
       const float2 z = unpack2(x[e]);
@@ -490,15 +491,15 @@ __device__ __forceinline__ void list_gradients(const DsArgs& a, const Slice<T>& 
 }
 
 template <typename T, typename D>
-__device__ __forceinline__ void put_gradients(D* d, bool aligned, const uint4& raw, float m,
-                                              float c, float coef) {
+__device__ __forceinline__ void put_gradients(D* d, bool aligned, const uint4& raw, bool wide,
+                                              float m, float c, float coef) {
   constexpr int NP = Vec<T>::VE / 2;
   uint64_t x[NP], g[NP];
   Vec<T>::get(raw, x);
   if (coef == 0.f) {                                   // whatever z holds
 #pragma unroll
     for (int e = 0; e < NP; ++e) g[e] = 0;
-  } else if (ds_wide(m, c)) {
+  } else if (wide) {
 #pragma unroll
     for (int e = 0; e < NP; ++e) {
       const float2 z = unpack2(x[e]);
@@ -530,11 +531,11 @@ __device__ __forceinline__ float ds_coef(float wt, float mass, float s) {
 template <typename T, typename D, int NV, int KPT>
 __global__ void __launch_bounds__(DS_THREADS, NV > 8 ? 2 : (KPT == 1 ? 4 : 3)) distill_hold_kernel(DsArgs a) {
   __shared__ DsShared sh;
-  const int64_t row = a.row0 + blockIdx.x / a.cl;
-  const int part = blockIdx.x % a.cl;
+  const int64_t row = a.row0 + blockIdx.y;
+  const int part = blockIdx.x;
   const int tid = threadIdx.x;
   const T* z = static_cast<const T*>(a.z) + row * a.ld_z;
-  const Slice<T> s(z, a.v, part, a.cl);
+  const Slice<T> s(z, a.v, part, a.per);
   uint4 raw[NV];
 #pragma unroll
   for (int n = 0; n < NV; ++n) {
@@ -551,10 +552,11 @@ __global__ void __launch_bounds__(DS_THREADS, NV > 8 ? 2 : (KPT == 1 ? 4 : 3)) d
   for (int n = 0; n < NV; ++n) rs.m = fmaxf(rs.m, Vec<T>::max(raw[n]));
   // a thread whose entries are all -inf adds nothing, to any reference (NaN it adds)
   const float m = rs.m == kNegInf ? 0.f : rs.m;
+  const bool mwide = ds_wide(m, a.c);
   uint64_t acc = pack2(ex2(ds_exponent(ze, m, a.c)), 0.f);
 #pragma unroll
   for (int n = 0; n < NV; ++n) {
-    acc = ds_terms<T>(acc, raw[n], m, a.c);
+    acc = ds_terms<T>(acc, raw[n], mwide, m, a.c);
     asm volatile("" : "+l"(acc));                      // one vector unpacked at a time
   }
   rs.s = unpack2(acc).x + unpack2(acc).y;
@@ -570,13 +572,13 @@ __global__ void __launch_bounds__(DS_THREADS, NV > 8 ? 2 : (KPT == 1 ? 4 : 3)) d
   int patch_id[KPT];
   list_gradients(a, s, e, rs, coef, wt, part, patch, patch_id);
   D* dz = static_cast<D*>(a.dz) + row * a.ld_dz;
-  const bool al = store_aligned(s, dz);
+  const bool al = store_aligned(s, dz), wide = ds_wide(rs.m, a.c);
 #pragma unroll
   for (int n = 0; n < NV; ++n) {
     const int i = s.i0 + tid + n * DS_THREADS;
     if (i < s.i1)
-      put_gradients<T, D>(dz + s.head + static_cast<int64_t>(i) * Vec<T>::VE, al, raw[n], rs.m, a.c,
-                          coef);
+      put_gradients<T, D>(dz + s.head + static_cast<int64_t>(i) * Vec<T>::VE, al, raw[n], wide,
+                          rs.m, a.c, coef);
   }
   put_edge(s, dz, ze, rs.m, a.c, coef);
   __syncthreads();
@@ -590,11 +592,11 @@ __global__ void __launch_bounds__(DS_THREADS, NV > 8 ? 2 : (KPT == 1 ? 4 : 3)) d
 template <typename T, typename D, bool LSE, bool GRAD, int KPT>
 __global__ void __launch_bounds__(DS_THREADS) distill_stream_kernel(DsArgs a) {
   __shared__ DsShared sh;
-  const int64_t row = a.row0 + blockIdx.x / a.cl;
-  const int part = blockIdx.x % a.cl;
+  const int64_t row = a.row0 + blockIdx.y;
+  const int part = blockIdx.x;
   const int tid = threadIdx.x;
   const T* z = static_cast<const T*>(a.z) + row * a.ld_z;
-  const Slice<T> s(z, a.v, part, a.cl);
+  const Slice<T> s(z, a.v, part, a.per);
   Entries<KPT> e;
   load_entries(a, row, s, part, LSE && part == 0, e);
   if (GRAD) clear_table(a);
@@ -617,9 +619,10 @@ __global__ void __launch_bounds__(DS_THREADS) distill_stream_kernel(DsArgs a) {
         rs.m = m;
       }
       if (!(m > kNegInf)) m = 0.f;                   // nothing but -inf (or NaN) so far
+      const bool mwide = ds_wide(m, a.c);
       uint64_t acc = 0;
 #pragma unroll
-      for (int u = 0; u < U; ++u) acc = ds_terms<T>(acc, raw[u], m, a.c);
+      for (int u = 0; u < U; ++u) acc = ds_terms<T>(acc, raw[u], mwide, m, a.c);
       rs.s += unpack2(acc).x + unpack2(acc).y;
     }
   } else {
@@ -641,7 +644,7 @@ __global__ void __launch_bounds__(DS_THREADS) distill_stream_kernel(DsArgs a) {
     int patch_id[KPT];
     list_gradients(a, s, e, rs, coef, wt, part, patch, patch_id);
     D* dz = static_cast<D*>(a.dz) + row * a.ld_dz;
-    const bool al = store_aligned(s, dz);
+    const bool al = store_aligned(s, dz), wide = ds_wide(rs.m, a.c);
     // dz may be z: every entry's z[id] was read before the first barrier above
     for (int i = s.i0 + tid; i < s.i1; i += U * DS_THREADS) {
       uint4 raw[U];
@@ -652,7 +655,7 @@ __global__ void __launch_bounds__(DS_THREADS) distill_stream_kernel(DsArgs a) {
       for (int u = 0; u < U; ++u)
         if (i + u * DS_THREADS < s.i1)
           put_gradients<T, D>(dz + s.head + static_cast<int64_t>(i + u * DS_THREADS) * Vec<T>::VE,
-                              al, raw[u], rs.m, a.c, coef);
+                              al, raw[u], wide, rs.m, a.c, coef);
     }
     put_edge(s, dz, ze, rs.m, a.c, coef);
     __syncthreads();
@@ -676,10 +679,9 @@ kronq_status launch_rows(void (*kern)(DsArgs), DsArgs a, int n, bool cluster, bo
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster && a.cl > 1 ? 1 : 0;
-  const int most = 0x7fffffff / a.cl;              // rows per launch: grid x extents end there
+  constexpr int most = 65535;                      // rows per launch: the grid's y extent
   for (a.row0 = 0; a.row0 < n; a.row0 += most) {
-    const int64_t rows = std::min<int64_t>(most, n - a.row0);
-    cfg.gridDim = dim3(static_cast<unsigned>(rows * a.cl));
+    cfg.gridDim = dim3(a.cl, static_cast<unsigned>(std::min<int64_t>(most, n - a.row0)));
     const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, a);
     if (err != cudaSuccess) return fail(KRONQ_ERR_CUDA, "%s: %s", what, cudaGetErrorString(err));
     KQ_TRY(check_launch(what));
@@ -694,7 +696,8 @@ kronq_status launch_distill(DsArgs a, int n, bool lse, bool grad, cudaStream_t s
   if (!lse) {
     // the gradient alone has no statistics to exchange: any number of slices, here of four
     // vectors per thread
-    a.cl = static_cast<int>((vecs + 4 * DS_THREADS - 1) / (4 * DS_THREADS));
+    a.per = 4 * DS_THREADS;
+    a.cl = static_cast<int>((vecs + a.per - 1) / a.per);
     return launch_rows(distill_stream_kernel<T, D, false, true, KPT>, a, n, false, true,
                        "distill_stream_kernel", stream);
   }
@@ -704,13 +707,15 @@ kronq_status launch_distill(DsArgs a, int n, bool lse, bool grad, cudaStream_t s
   while (a.cl < DS_MAX_CL && static_cast<int64_t>(n) * a.cl < 2 * device_sms() &&
          vecs > static_cast<int64_t>(a.cl) * DS_THREADS)
     a.cl *= 2;
+  auto cut = [&] { return static_cast<int>((vecs + a.cl - 1) / a.cl); };
+  a.per = cut();
   if (!grad)
     return launch_rows(distill_stream_kernel<T, D, true, false, KPT>, a, n, true, false,
                        "distill_stream_kernel", stream);
   while (a.cl < DS_MAX_CL && vecs > static_cast<int64_t>(a.cl) * DS_THREADS * NV) a.cl *= 2;
-  const int64_t per = (vecs + a.cl - 1) / a.cl;
-  auto kern = per <= DS_THREADS * NV       ? distill_hold_kernel<T, D, NV, KPT>
-              : per <= DS_THREADS * 2 * NV ? distill_hold_kernel<T, D, 2 * NV, KPT>
+  a.per = cut();
+  auto kern = a.per <= DS_THREADS * NV       ? distill_hold_kernel<T, D, NV, KPT>
+              : a.per <= DS_THREADS * 2 * NV ? distill_hold_kernel<T, D, 2 * NV, KPT>
                                            : distill_stream_kernel<T, D, true, true, KPT>;
   return launch_rows(kern, a, n, true, true, "distill kernel", stream);
 }
