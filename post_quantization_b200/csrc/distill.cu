@@ -10,13 +10,19 @@
 // rounding of m c is the same in a row's sum and in its q, where it cancels, and lse undoes it.
 // Where m c overflows (a row that holds nothing but the type's lowest value) the exponent is
 // (z - m) c instead.
-// Per element and use of z: an unpack, half a packed fp32 FMA, one ex2, half a packed fp32 add or
-// multiply. The two ex2 of loss + gradient (16 a cycle and SM) stay below the time of the bytes.
+// Per element: an unpack, half a packed fp32 FMA, one ex2 (16 a cycle and SM), half a packed add.
 //
 // A row is cut into cl slices of 16-byte vectors, one CTA each. Where the row's statistics are
 // needed the CTAs of a row form a cluster and exchange (m, s) through distributed shared memory.
-//   distill_hold_kernel     loss and gradient in one read: a thread keeps its vectors of z in
-//                           registers between the statistics and the gradient
+//   distill_ring_kernel     loss and gradient of long rows in one read. Persistent clusters, two
+//                           CTAs per SM so that one's barriers hide behind the other's work. A
+//                           producer warp fetches chunks of the CTA's slices, row after row, into
+//                           a ring in shared memory (bulk copies); eight warps take the statistics
+//                           as chunks arrive, keep the row there, and free each chunk as its
+//                           gradient is written, so that the next row's reads go on; two list warps
+//                           do all that concerns the teacher's entries, for rows in turn
+//   distill_hold_kernel     loss and gradient of short rows, or of few: a thread keeps its vectors
+//                           of z in registers between the statistics and the gradient
 //   distill_stream_kernel   the loss alone, the gradient from a given lse, and loss + gradient of
 //                           rows too long to hold (which are then read twice)
 // Listed entries are few: their p, their part of the loss and their gradients are computed by
@@ -35,8 +41,11 @@ namespace {
 
 constexpr int DS_THREADS = 256;
 constexpr int DS_WARPS = DS_THREADS / 32;
-constexpr int DS_KPT_MAX = kMaxDistillTop / DS_THREADS;   // listed entries per thread
+constexpr int DS_RING_THREADS = DS_THREADS + 96;      // ring kernel: a producer and two list warps
 constexpr int DS_MAX_CL = 8;                          // CTAs per row (portable cluster size)
+constexpr int DS_CHUNK_VECS = 4 * DS_THREADS;         // vectors per ring chunk (16 KB)
+constexpr int DS_MAX_CHUNKS = 13;                     // chunks in the ring
+constexpr int DS_RING_MIN_VECS = 2048;                // rows below 32 KB do not use the ring
 constexpr float kNegInf = -INFINITY;
 
 struct DsArgs {
@@ -179,10 +188,21 @@ struct Slice {
     const int i = (e - head) / Vec<T>::VE;
     return i >= i0 && i < i1;
   }
-  __device__ __forceinline__ uint4 load(int i) const {
-    return ds_ldg(row + head + static_cast<int64_t>(i) * Vec<T>::VE);
+  __device__ __forceinline__ const T* at(int i) const {
+    return row + head + static_cast<int64_t>(i) * Vec<T>::VE;
   }
+  __device__ __forceinline__ uint4 load(int i) const { return ds_ldg(at(i)); }
 };
+
+// Bulk copy global -> shared, completion on `bar` (no multicast); 16-byte addresses and size.
+__device__ __forceinline__ void ds_bulk_load(void* dst, const void* src, uint32_t bytes,
+                                             uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
 
 // Stores a vector's gradients at d: as 8- or 16-byte words where aligned, else one by one.
 template <typename D, int VE>
@@ -223,7 +243,7 @@ __device__ __forceinline__ bool store_aligned(const Slice<T>& s, const D* dz) {
 }
 
 // Running maximum and sum of 2^(z c - fl(m c)). m = -inf, s = 0: nothing but -inf seen.
-struct RunSum {
+struct __align__(8) RunSum {      // sent as one 8-byte word
   float m, s;
 };
 __device__ __forceinline__ bool ds_wide(float m, float c) { return !(fabsf(m * c) < INFINITY); }
@@ -245,28 +265,38 @@ __device__ __forceinline__ RunSum ds_join_lanes(RunSum r, float c) {
   for (int o = W / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   return {m, s};
 }
-// acc += the terms of one vector against a maximum that covers it
-template <typename T>
-__device__ __forceinline__ uint64_t ds_terms(uint64_t acc, const uint4& raw, bool wide, float m,
-                                             float c) {
+// The sum of the terms of U vectors against a reference m. One branch for all of them: the
+// exponentials of different vectors overlap only within one straight run of code.
+template <typename T, int U>
+__device__ __forceinline__ float ds_terms(const uint4 (&raw)[U], bool wide, float m, float c) {
   constexpr int NP = Vec<T>::VE / 2;
-  uint64_t x[NP];
-  Vec<T>::get(raw, x);
+  uint64_t acc[2] = {0, 0};                          // two chains of packed sums
   if (wide) {
 #pragma unroll
-    for (int e = 0; e < NP; ++e) {
-      const float2 z = unpack2(x[e]);
-      acc = add2(acc, pack2(ex2((z.x - m) * c), ex2((z.y - m) * c)));
+    for (int u = 0; u < U; ++u) {
+      uint64_t x[NP];
+      Vec<T>::get(raw[u], x);
+#pragma unroll
+      for (int e = 0; e < NP; ++e) {
+        const float2 z = unpack2(x[e]);
+        acc[0] = add2(acc[0], pack2(ex2((z.x - m) * c), ex2((z.y - m) * c)));
+      }
     }
   } else {
     const uint64_t cc = pack2(c, c), ref = pack2(-(m * c), -(m * c));
 #pragma unroll
-    for (int e = 0; e < NP; ++e) {
-      const float2 d = unpack2(fma2(x[e], cc, ref));
-      acc = add2(acc, pack2(ex2(d.x), ex2(d.y)));
+    for (int u = 0; u < U; ++u) {
+      uint64_t x[NP];
+      Vec<T>::get(raw[u], x);
+#pragma unroll
+      for (int e = 0; e < NP; ++e) {
+        const float2 d = unpack2(fma2(x[e], cc, ref));
+        acc[e & 1] = add2(acc[e & 1], pack2(ex2(d.x), ex2(d.y)));
+      }
     }
   }
-  return acc;
+  const float2 s = unpack2(add2(acc[0], acc[1]));
+  return s.x + s.y;
 }
 
 __device__ __forceinline__ void ds_cluster_arrive() {
@@ -274,6 +304,17 @@ __device__ __forceinline__ void ds_cluster_arrive() {
 }
 __device__ __forceinline__ void ds_cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Eight bytes into a peer's shared memory, counted on a barrier there.
+__device__ __forceinline__ void ds_send(const RunSum* dst, const uint64_t* bar, uint32_t rank,
+                                        RunSum v) {
+  uint32_t a, b;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(dst)), "r"(rank));
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(smem_u32(bar)), "r"(rank));
+  asm volatile(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(a),
+      "l"(pack2(v.m, v.s)), "r"(b)
+      : "memory");
 }
 __device__ __forceinline__ float ds_remote(const void* p, uint32_t rank) {
   uint32_t a;
@@ -284,66 +325,86 @@ __device__ __forceinline__ float ds_remote(const void* p, uint32_t rank) {
 }
 
 struct DsShared {
-  RunSum row[DS_WARPS];          // statistics per warp
-  RunSum list[DS_WARPS];         // and of the listed logits
+  RunSum row[DS_WARPS];      // statistics per warp
+  RunSum list[DS_WARPS];     // and of the listed logits
   RunSum mine;                   // this CTA's statistics, read by the cluster
   double loss[DS_WARPS];
   float mass[DS_WARPS];
+  float z[kMaxDistillTop];       // the listed entries' z
+  int repeated;                  // an id is listed twice
 };
 
-// With a gradient, in dynamic shared memory: the list, for repeated ids, and a table from an id to
-// the first j that lists it and how many do.
+// With a gradient, in dynamic shared memory: the list, and a table that finds out whether an id is
+// listed twice. Only then are the lists searched: the first j that lists an id adds up all its p,
+// in the order of the list.
 struct IdTable {
   float* p;                      // k
-  int* id;                       // k
-  int* key;                      // hash_mask + 1 each
-  int* first;
-  int* count;
-  __device__ __forceinline__ explicit IdTable(const DsArgs& a) {
-    extern __shared__ int ds_table[];
-    key = ds_table;
-    first = key + a.hash_mask + 1;
-    count = first + a.hash_mask + 1;
-    id = count + a.hash_mask + 1;
+  int* id;                       // k; -1: absent
+  int* slot;                     // hash_mask + 1: j of the entry that took the slot, or -1
+  __device__ __forceinline__ IdTable(const DsArgs& a, int* mem) {
+    slot = mem;
+    id = slot + a.hash_mask + 1;
     p = reinterpret_cast<float*>(id + a.k);
   }
+  // Enters entry j; true where its id was there already. Every id[] is written before.
+  __device__ __forceinline__ bool insert(const DsArgs& a, int j) const {
+    uint32_t h = (static_cast<uint32_t>(id[j]) * 2654435761u >> 16) & a.hash_mask;
+    while (true) {               // at most k of >= 2 k slots are taken
+      const int old = atomicCAS(&slot[h], -1, j);
+      if (old == -1) return false;
+      if (id[old] == id[j]) return true;
+      h = (h + 1) & a.hash_mask;
+    }
+  }
+  // P of entry j's id, or -1 where an earlier entry lists it
+  __device__ __forceinline__ float total(const DsArgs& a, int j) const {
+    for (int l = 0; l < j; ++l)
+      if (id[l] == id[j]) return -1.f;
+    float sum = p[j];
+    for (int l = j + 1; l < a.k; ++l)
+      if (id[l] == id[j]) sum += p[l];
+    return sum;
+  }
 };
-size_t id_table_bytes(const DsArgs& a) {
-  return (3 * (static_cast<size_t>(a.hash_mask) + 1) + 2 * static_cast<size_t>(a.k)) * 4;
+__host__ __device__ inline int id_table_words(const DsArgs& a) {
+  return a.hash_mask + 1 + 2 * a.k;
 }
 
-// The listed entries of a row: thread t has entries t, t + 256, ... (KPT of them)
+// The listed entries of a row: thread t has entries t, t + NT, ... (KPT of them)
 template <int KPT>
 struct Entries {
   int id[KPT];                   // -1: absent
   float t[KPT], z[KPT], p[KPT];
 };
 
-__device__ __forceinline__ uint32_t ds_slot(const DsArgs& a, int id) {
-  return (static_cast<uint32_t>(id) * 2654435761u >> 16) & a.hash_mask;
+template <int NT, int KPT>
+__device__ __forceinline__ void load_entries(const DsArgs& a, int64_t row, Entries<KPT>& e) {
+#pragma unroll
+  for (int i = 0; i < KPT; ++i) {
+    const int j = threadIdx.x + i * NT;
+    e.id[i] = -1;
+    e.t[i] = kNegInf;
+    if (j < a.k) {
+      const int id = a.ids[row * a.ld_ids + j];
+      const int64_t o = row * a.ld_top + j;
+      const float t = a.top_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.top)[o])
+                                 : static_cast<const float*>(a.top)[o];
+      if (id >= 0 && id < a.v) {
+        e.id[i] = id;
+        e.t[i] = t;
+      }
+    }
+  }
 }
-
 // z[id] is read where it is used: for the loss (all entries), and for the gradients of the entries
 // in the CTA's own slice (other slices may already be overwritten when dz is z).
 template <typename T, int KPT>
-__device__ __forceinline__ void load_entries(const DsArgs& a, int64_t row, const Slice<T>& s,
-                                             int part, bool all, Entries<KPT>& e) {
+__device__ __forceinline__ void gather_logits(const Slice<T>& s, int part, bool all,
+                                              Entries<KPT>& e) {
 #pragma unroll
   for (int i = 0; i < KPT; ++i) {
-    const int j = threadIdx.x + i * DS_THREADS;
-    e.id[i] = -1;
-    e.t[i] = kNegInf;
     e.z[i] = 0.f;
-    if (j < a.k) {
-      const int id = a.ids[row * a.ld_ids + j];
-      if (id >= 0 && id < a.v) {
-        const int64_t o = row * a.ld_top + j;
-        e.id[i] = id;
-        e.t[i] = a.top_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.top)[o])
-                            : static_cast<const float*>(a.top)[o];
-        if (all || s.owns(id, part)) e.z[i] = ds_ld(s.row + id);
-      }
-    }
+    if (e.id[i] >= 0 && (all || s.owns(e.id[i], part))) e.z[i] = ds_ld(s.row + e.id[i]);
   }
 }
 
@@ -352,12 +413,15 @@ __device__ __forceinline__ double ds_lse(const DsArgs& a, RunSum r) {
   return (ds_wide(r.m, a.c) ? r.m * a.inv_tau : r.m * a.c * a.nat) + logf(r.s);
 }
 
-// Joins the CTA's (and, with a cluster, the row's) statistics and the listed entries'; gives p and,
-// in the CTA that reports the row, the loss. GRAD: fills the id table.
-template <bool LSE, bool GRAD, int KPT>
+// Joins the CTA's statistics, the row's (exchange: what other CTAs have) and the listed entries';
+// gives p and, in the CTA that reports the row, the loss. GRAD: fills the id table. sync(): a
+// barrier of the NT threads.
+template <int NT, bool LSE, bool GRAD, int KPT, typename Sync, typename Exchange>
 __device__ __forceinline__ void row_statistics(const DsArgs& a, int64_t row, int part, float w,
-                                               DsShared& sh, RunSum& rs, Entries<KPT>& e,
-                                               float& mass) {
+                                               float top_lse, DsShared& sh, int* table_mem,
+                                               RunSum& rs, Entries<KPT>& e, float& mass, Sync sync,
+                                               Exchange exchange) {
+  constexpr int NW = NT / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool lists = warp * 32 < a.k;            // some thread of the warp has an entry
   if (LSE) {
@@ -373,34 +437,39 @@ __device__ __forceinline__ void row_statistics(const DsArgs& a, int64_t row, int
       if (e.t[i] != kNegInf) ls.s += ex2(ds_exponent(e.t[i], ls.m == kNegInf ? 0.f : ls.m, a.c));
     ls = ds_join_lanes<32>(ls, a.c);
   }
+  const bool report = LSE && part == 0;
   if (lane == 0) sh.list[warp] = ls;
-  __syncthreads();
+  // z[id] has arrived before any other CTA learns of this one's statistics and stores its part
+  // of the row (dz may be z)
+  if (report && lists) {
+#pragma unroll
+    for (int i = 0; i < KPT; ++i)
+      if (tid + i * NT < a.k) *const_cast<volatile float*>(&sh.z[tid + i * NT]) = e.z[i];
+  }
+  if (GRAD) {
+    const IdTable table(a, table_mem);
+#pragma unroll
+    for (int i = 0; i < KPT; ++i)
+      if (tid + i * NT < a.k) table.id[tid + i * NT] = e.id[i];
+    if (tid == 0) sh.repeated = 0;
+  }
+  sync();
   if (LSE) {
-    rs = ds_join_lanes<DS_WARPS>(sh.row[lane % DS_WARPS], a.c);
-    if (a.cl > 1) {
-      if (tid == 0) sh.mine = rs;
-      ds_cluster_arrive();
-      ds_cluster_wait();
-      const int r = lane % DS_MAX_CL;
-      rs = {kNegInf, 0.f};
-      if (r < a.cl) rs = {ds_remote(&sh.mine.m, r), ds_remote(&sh.mine.s, r)};
-      rs = ds_join_lanes<DS_MAX_CL>(rs, a.c);
-      ds_cluster_arrive();                         // waited for before the CTA ends
-    }
+    rs = ds_join_lanes<NW>(sh.row[lane % NW], a.c);
+    if (a.cl > 1) rs = exchange(rs);
   }
   double part_loss = 0.0;
-  const bool report = LSE && part == 0;
   const double lse = report ? ds_lse(a, rs) : 0.0;
   mass = 0.f;
 #pragma unroll
   for (int i = 0; i < KPT; ++i) e.p[i] = 0.f;
   if (lists) {
     // log p_j = t_j / tau - L_t in fp64: the difference of two numbers of the logits' size
-    ls = ds_join_lanes<DS_WARPS>(sh.list[lane % DS_WARPS], a.c);
-    const double norm = a.top_lse ? static_cast<double>(a.top_lse[row]) : ds_lse(a, ls);
+    ls = ds_join_lanes<NW>(sh.list[lane % NW], a.c);
+    const double norm = a.top_lse ? static_cast<double>(top_lse) : ds_lse(a, ls);
 #pragma unroll
     for (int i = 0; i < KPT; ++i) {
-      const int j = tid + i * DS_THREADS;
+      const int j = tid + i * NT;
       if (j >= a.k) break;
       if (e.t[i] != kNegInf) {
         const double lp = e.t[i] * a.inv_tau - norm;
@@ -413,19 +482,9 @@ __device__ __forceinline__ void row_statistics(const DsArgs& a, int64_t row, int
                                          : p * (lp - e.z[i] * a.inv_tau + lse);
       }
       if (GRAD) {
-        const IdTable table(a);
+        const IdTable table(a, table_mem);
         table.p[j] = e.p[i];
-        table.id[j] = e.id[i];
-        if (e.id[i] >= 0) {
-          uint32_t h = ds_slot(a, e.id[i]);
-          while (true) {                           // at most k of >= 2 k slots are taken
-            const int old = atomicCAS(&table.key[h], -1, e.id[i]);
-            if (old == -1 || old == e.id[i]) break;
-            h = (h + 1) & a.hash_mask;
-          }
-          atomicMin(&table.first[h], j);
-          atomicAdd(&table.count[h], 1);
-        }
+        if (e.id[i] >= 0 && table.insert(a, j)) sh.repeated = 1;
       }
     }
     __syncwarp();
@@ -440,80 +499,107 @@ __device__ __forceinline__ void row_statistics(const DsArgs& a, int64_t row, int
     sh.mass[warp] = mass;
     if (report) sh.loss[warp] = part_loss;
   }
-  __syncthreads();
+  sync();
   mass = 0.f;
 #pragma unroll
-  for (int i = 0; i < DS_WARPS; ++i) mass += sh.mass[i];
+  for (int i = 0; i < NW; ++i) mass += sh.mass[i];
   if (report && tid == 0) {
     double tot = 0.0;
-    for (int i = 0; i < DS_WARPS; ++i) tot += sh.loss[i];
+    for (int i = 0; i < NW; ++i) tot += sh.loss[i];
     a.loss[row] = w == 0.f ? 0.f : static_cast<float>(static_cast<double>(w) * a.tau * a.tau * tot);
     if (a.lse) a.lse[row] = static_cast<float>(lse);
   }
 }
 
-__device__ __forceinline__ void clear_table(const DsArgs& a) {
-  const IdTable table(a);
-  for (int i = threadIdx.x; i <= a.hash_mask; i += DS_THREADS) {
-    table.key[i] = -1;
-    table.first[i] = kMaxDistillTop;
-    table.count[i] = 0;
-  }
+// The row's statistics from those of the cluster's CTAs. The second arrival is waited for before
+// the CTA ends.
+__device__ __forceinline__ RunSum exchange_cluster(const DsArgs& a, DsShared& sh, RunSum mine) {
+  if (threadIdx.x == 0) sh.mine = mine;
+  ds_cluster_arrive();
+  ds_cluster_wait();
+  const int r = (threadIdx.x & 31) % DS_MAX_CL;
+  RunSum all{kNegInf, 0.f};
+  if (r < a.cl) all = {ds_remote(&sh.mine.m, r), ds_remote(&sh.mine.s, r)};
+  all = ds_join_lanes<DS_MAX_CL>(all, a.c);
+  ds_cluster_arrive();
+  return all;
 }
 
-// Gradients of the listed entries in this CTA's slice: the first thread that lists an id adds up
-// all its p, in the order of the list. patch_id = -1: not this thread's to store.
-template <typename T, int KPT>
-__device__ __forceinline__ void list_gradients(const DsArgs& a, const Slice<T>& s,
-                                               const Entries<KPT>& e, RunSum rs, float coef,
-                                               float wt, int part, float (&patch)[KPT],
-                                               int (&patch_id)[KPT]) {
-  const IdTable table(a);
+template <int NT>
+__device__ __forceinline__ void clear_table(const DsArgs& a, int* table_mem) {
+  const IdTable table(a, table_mem);
+  for (int i = threadIdx.x; i <= a.hash_mask; i += NT) table.slot[i] = -1;
+}
+
+// Gradients of the listed entries in this CTA's slice. patch_id = -1: not this thread's to store.
+template <int NT, typename T, int KPT>
+__device__ __forceinline__ void list_gradients(const DsArgs& a, const DsShared& sh,
+                                               const Slice<T>& s, const Entries<KPT>& e, RunSum rs,
+                                               float coef, float wt, int part, int* table_mem,
+                                               float (&patch)[KPT], int (&patch_id)[KPT]) {
+  const IdTable table(a, table_mem);
 #pragma unroll
   for (int i = 0; i < KPT; ++i) {
-    const int j = threadIdx.x + i * DS_THREADS;
+    const int j = threadIdx.x + i * NT;
     patch_id[i] = -1;
     patch[i] = 0.f;
     if (j < a.k && e.id[i] >= 0 && s.owns(e.id[i], part)) {
-      uint32_t h = ds_slot(a, e.id[i]);
-      while (table.key[h] != e.id[i]) h = (h + 1) & a.hash_mask;
-      if (table.first[h] == j) {
-        float p = e.p[i];
-        if (table.count[h] > 1)
-          for (int l = j + 1; l < a.k; ++l)
-            if (table.id[l] == e.id[i]) p += table.p[l];
+      const float p = sh.repeated ? table.total(a, j) : e.p[i];
+      if (p >= 0.f || p != p) {
         patch_id[i] = e.id[i];
         if (wt != 0.f)
-          patch[i] = coef == 0.f ? -wt * p : fmaf(coef, ex2(ds_exponent(e.z[i], rs.m, a.c)), -wt * p);
+          patch[i] = coef == 0.f ? -wt * p
+                                 : fmaf(coef, ex2(ds_exponent(e.z[i], rs.m, a.c)), -wt * p);
       }
     }
   }
 }
 
-template <typename T, typename D>
-__device__ __forceinline__ void put_gradients(D* d, bool aligned, const uint4& raw, bool wide,
-                                              float m, float c, float coef) {
+// Gradients of U vectors, `stride` elements apart from d on; vector u is stored where u < have.
+template <typename T, typename D, int U>
+__device__ __forceinline__ void put_gradients(D* d, int64_t stride, int have, bool aligned,
+                                              const uint4 (&raw)[U], bool wide, float m, float c,
+                                              float coef) {
   constexpr int NP = Vec<T>::VE / 2;
-  uint64_t x[NP], g[NP];
-  Vec<T>::get(raw, x);
+  uint64_t g[U][NP];
   if (coef == 0.f) {                                   // whatever z holds
 #pragma unroll
-    for (int e = 0; e < NP; ++e) g[e] = 0;
-  } else if (wide) {
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-    for (int e = 0; e < NP; ++e) {
-      const float2 z = unpack2(x[e]);
-      g[e] = pack2(coef * ex2((z.x - m) * c), coef * ex2((z.y - m) * c));
-    }
+      for (int e = 0; e < NP; ++e) g[u][e] = 0;
   } else {
-    const uint64_t cc = pack2(c, c), ref = pack2(-(m * c), -(m * c)), k = pack2(coef, coef);
+    const uint64_t cc = pack2(c, c), k = pack2(coef, coef);
+    const float r = wide ? -m : -(m * c);
+    const uint64_t ref = pack2(r, r);
 #pragma unroll
-    for (int e = 0; e < NP; ++e) {
-      const float2 t = unpack2(fma2(x[e], cc, ref));
-      g[e] = mul2(k, pack2(ex2(t.x), ex2(t.y)));
+    for (int u = 0; u < U; ++u) {
+      uint64_t x[NP];
+      Vec<T>::get(raw[u], x);
+#pragma unroll
+      for (int e = 0; e < NP; ++e) g[u][e] = x[e];
     }
+    if (wide) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < NP; ++e) g[u][e] = mul2(add2(g[u][e], ref), cc);
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < NP; ++e) g[u][e] = fma2(g[u][e], cc, ref);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < NP; ++e) {
+        const float2 t = unpack2(g[u][e]);
+        g[u][e] = mul2(k, pack2(ex2(t.x), ex2(t.y)));
+      }
   }
-  store_vec<D, Vec<T>::VE>(d, aligned, g);
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (u < have) store_vec<D, Vec<T>::VE>(d + u * stride, aligned, g[u]);
 }
 template <typename T, typename D>
 __device__ __forceinline__ void put_edge(const Slice<T>& s, D* dz, float z, float m, float c,
@@ -525,6 +611,302 @@ __device__ __forceinline__ void put_edge(const Slice<T>& s, D* dz, float z, floa
 // holds nothing but -inf
 __device__ __forceinline__ float ds_coef(float wt, float mass, float s) {
   return (wt == 0.f || mass == 0.f || s == 0.f) ? 0.f : wt * mass / s;
+}
+
+// Loss and gradient of long rows. Cluster y takes rows y, y + gridDim.y, ...; chunk g of the CTA
+// (its slices' chunks, row after row) sits in ring slot g % chunks.
+//
+// Per row: every consumer warp sends its statistics to all CTAs of the cluster and waits for all of
+// theirs (8 warps x cl messages on barrier got). Rows alternate between two of each barrier and
+// buffer (turn): a message for the next row may come before this row's last, one for the row after
+// that is sent only when this CTA has sent its next, and it sends that only when its list warp too
+// has read this row's (barrier taken). The list warp gives P and z[id] (barrier ready)
+// before the CTA's first warp sends: no CTA stores a part of the row (dz may be z) before every
+// z[id] of it is read. It stores the listed entries' gradients when the warps have stored the row's
+// (barrier stored).
+template <typename T, typename D>
+__global__ void __launch_bounds__(DS_RING_THREADS, 2)
+    distill_ring_kernel(DsArgs a, int64_t n, int chunks, int* err) {
+  constexpr int VE = Vec<T>::VE, U = DS_CHUNK_VECS / DS_THREADS;
+  constexpr uint32_t CHUNK = DS_CHUNK_VECS * 16;
+  extern __shared__ __align__(128) uint8_t ds_ring[];
+  __shared__ RunSum stats[2][DS_WARPS * DS_MAX_CL];
+  __shared__ float masses[2];
+  __shared__ __align__(8) uint64_t full[DS_MAX_CHUNKS], empty[DS_MAX_CHUNKS], got[2], ready[2],
+      taken[2], stored[2];
+  __shared__ int abort_flag;
+  const int part = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t step = gridDim.y;
+  auto slice = [&](int64_t row) {
+    return Slice<T>(static_cast<const T*>(a.z) + row * a.ld_z, a.v, part, a.per);
+  };
+  if (tid == 0) {
+    for (int i = 0; i < chunks; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], DS_WARPS);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&got[i], a.cl > 1 ? 1 : DS_WARPS);
+      mbar_init(&ready[i], 1);
+      mbar_init(&taken[i], 1);
+      mbar_init(&stored[i], DS_WARPS);
+    }
+    abort_flag = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  if (a.cl > 1) {                                     // peers' barriers exist before any message
+    ds_cluster_arrive();
+    ds_cluster_wait();
+  }
+  volatile int* const aborted = &abort_flag;
+  // the row's statistics from the messages
+  auto joined = [&](int turn) {
+    const int all = a.cl * DS_WARPS;
+    RunSum r{kNegInf, 0.f}, r2{kNegInf, 0.f};
+    if (lane < all) r = stats[turn][lane];
+    if (lane + 32 < all) r2 = stats[turn][lane + 32];
+    const float m = fmaxf(r.m, r2.m);
+    const float f = r.m == m ? 1.f : ds_rescale(r.m, m, a.c);
+    const float f2 = r2.m == m ? 1.f : ds_rescale(r2.m, m, a.c);
+    return ds_join_lanes<32>({m, r.s * f + r2.s * f2}, a.c);
+  };
+  // After a wait that gave up (recorded in err) the roles run on over whatever shared memory holds:
+  // every later wait returns at once.
+  if (warp == DS_WARPS) {
+    // ------------------------------------------------------------------ producer
+    if (lane == 0) {
+      int slot = 0;
+      uint32_t parity = 1, issued = 0;                // a fresh barrier's previous phase is over
+      bool ok = true;
+      for (int64_t row = blockIdx.y; row < n && ok; row += step) {
+        const Slice<T> s = slice(row);
+        for (int i = s.i0; i < s.i1; i += DS_CHUNK_VECS) {
+          if (!mbar_wait(&empty[slot], parity, aborted, err, DEV_ERR_TMA_WAIT)) {
+            ok = false;
+            break;
+          }
+          const uint32_t bytes = static_cast<uint32_t>(min(DS_CHUNK_VECS, s.i1 - i)) * 16;
+          mbar_arrive_expect_tx(&full[slot], bytes);
+          ds_bulk_load(ds_ring + slot * CHUNK, s.at(i), bytes, &full[slot]);
+          ++issued;
+          if (++slot == chunks) {
+            slot = 0;
+            parity ^= 1u;
+          }
+        }
+      }
+      if (*aborted) {                                 // copies in flight land before the CTA ends
+        const uint32_t ring = chunks;
+        for (uint32_t g = issued > ring ? issued - ring : 0; g < issued; ++g)
+          mbar_drain(&full[g % ring], (g / ring) & 1u, 1000000000ull);
+      }
+    }
+  } else if (warp > DS_WARPS) {
+    // ------------------------------------------------------------------ the teacher's lists
+    const int turn = warp - DS_WARPS - 1;             // this warp's rows
+    const IdTable table(a, reinterpret_cast<int*>(ds_ring + chunks * CHUNK) +
+                               turn * (id_table_words(a) + 4 * a.k));
+    float* const t = table.p + a.k;                   // logits (-inf: absent), z[id]
+    float* const zk = t + a.k;
+    int* const own = reinterpret_cast<int*>(zk + a.k);       // id where it lies in this CTA's slice
+    float* const grad = reinterpret_cast<float*>(own + a.k);
+    uint32_t parity = 0;
+    for (int64_t row = blockIdx.y + turn * step; row < n; row += 2 * step, parity ^= 1u) {
+      const Slice<T> s = slice(row);
+      const float w = a.weight ? a.weight[row] : 1.f;
+      const float wt = w * a.tau;
+      for (int i = lane; i <= a.hash_mask; i += 32) table.slot[i] = -1;
+      RunSum ls{kNegInf, 0.f};
+      constexpr int B = 4;                            // entries per lane with loads in flight
+      for (int j0 = lane; j0 < a.k; j0 += 32 * B) {
+        int id[B];
+        float x[B], z[B];
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+          const int j = j0 + 32 * b;
+          id[b] = -1;
+          x[b] = kNegInf;
+          if (j < a.k) {
+            id[b] = a.ids[row * a.ld_ids + j];
+            const int64_t o = row * a.ld_top + j;
+            x[b] = a.top_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.top)[o])
+                              : static_cast<const float*>(a.top)[o];
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+          if (id[b] < 0 || id[b] >= a.v) {
+            id[b] = -1;
+            x[b] = kNegInf;
+          }
+          z[b] = id[b] >= 0 && (part == 0 || s.owns(id[b], part)) ? ds_ld(s.row + id[b]) : 0.f;
+          ls.m = fmaxf(ls.m, x[b]);
+        }
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+          const int j = j0 + 32 * b;
+          if (j < a.k) {
+            zk[j] = z[b];
+            table.id[j] = id[b];
+            t[j] = x[b];
+            own[j] = id[b] >= 0 && s.owns(id[b], part) ? id[b] : -1;
+          }
+        }
+      }
+      for (int j = lane; j < a.k; j += 32)            // a NaN logit makes s NaN
+        if (t[j] != kNegInf) ls.s += ex2(ds_exponent(t[j], ls.m == kNegInf ? 0.f : ls.m, a.c));
+      ls = ds_join_lanes<32>(ls, a.c);
+      // log p_j = t_j / tau - L_t in fp64: the difference of two numbers of the logits' size
+      const double norm = a.top_lse ? static_cast<double>(a.top_lse[row]) : ds_lse(a, ls);
+      float mass = 0.f;
+      for (int j = lane; j < a.k; j += 32) {
+        const float p = t[j] == kNegInf ? 0.f : expf(static_cast<float>(t[j] * a.inv_tau - norm));
+        table.p[j] = p;
+        mass += p;
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
+      if (lane == 0) {
+        masses[turn] = mass;
+        mbar_arrive(&ready[turn]);
+      }
+      __syncwarp();
+      bool again = false;
+      for (int j = lane; j < a.k; j += 32)
+        if (table.id[j] >= 0) again |= table.insert(a, j);
+      again = __any_sync(0xffffffffu, again);
+      if (again) {
+        for (int j = lane; j < a.k; j += 32) {
+          if (own[j] < 0) continue;
+          const float p = table.total(a, j);
+          if (p < 0.f) own[j] = -1;
+          grad[j] = p;
+        }
+      }
+      mbar_wait(&got[turn], parity, aborted, err, DEV_ERR_EPI_WAIT);
+      const RunSum rs = joined(turn);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&taken[turn]);
+      const float coef = ds_coef(wt, mass, rs.s);
+      for (int j = lane; j < a.k; j += 32) {
+        if (own[j] < 0) continue;
+        const float p = again ? grad[j] : table.p[j];
+        grad[j] = wt == 0.f ? 0.f
+                            : (coef == 0.f ? -wt * p
+                                           : fmaf(coef, ex2(ds_exponent(zk[j], rs.m, a.c)), -wt * p));
+      }
+      if (part == 0) {
+        const double lse = ds_lse(a, rs);
+        double loss = 0.0;
+        for (int j = lane; j < a.k; j += 32)
+          if (table.p[j] != 0.f)                      // a masked listed entry: infinite loss
+            loss += zk[j] == kNegInf ? static_cast<double>(INFINITY)
+                                     : table.p[j] * ((static_cast<double>(t[j]) - zk[j]) * a.inv_tau - norm + lse);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, o);
+        if (lane == 0) {
+          a.loss[row] = w == 0.f ? 0.f
+                                 : static_cast<float>(static_cast<double>(w) * a.tau * a.tau * loss);
+          if (a.lse) a.lse[row] = static_cast<float>(lse);
+        }
+      }
+      mbar_wait(&stored[turn], parity, aborted, err, DEV_ERR_EPI_WAIT);
+      D* dz = static_cast<D*>(a.dz) + row * a.ld_dz;
+      for (int j = lane; j < a.k; j += 32)
+        if (own[j] >= 0) ds_st(dz + own[j], grad[j]);
+      __syncwarp();
+    }
+  } else {
+    // ------------------------------------------------------------------ consumers
+    int slot = 0, turn = 0;
+    uint32_t full_parity = 0, parity = 0;
+    for (int64_t row = blockIdx.y; row < n; row += step) {
+      const Slice<T> s = slice(row);
+      if (tid == 0 && a.cl > 1) mbar_arrive_expect_tx(&got[turn], 8 * DS_WARPS * a.cl);
+      const float w = a.weight ? a.weight[row] : 1.f;
+      const float ze = s.edge >= 0 ? ds_ld(s.row + s.edge) : kNegInf;
+      const int slot0 = slot;
+      RunSum rs{kNegInf, 0.f};
+      for (int i = s.i0; i < s.i1; i += DS_CHUNK_VECS) {
+        mbar_wait(&full[slot], full_parity, aborted, err, DEV_ERR_LOAD_WAIT);
+        const uint4* ring = reinterpret_cast<const uint4*>(ds_ring + slot * CHUNK) + tid;
+        uint4 raw[U];
+        if (i + DS_CHUNK_VECS <= s.i1) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) raw[u] = ring[u * DS_THREADS];
+        } else {
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            raw[u] = i + tid + u * DS_THREADS < s.i1 ? ring[u * DS_THREADS] : none_vec<T>();
+        }
+        float most = kNegInf;
+#pragma unroll
+        for (int u = 0; u < U; ++u) most = fmaxf(most, Vec<T>::max(raw[u]));
+        // the thread's reference changes only where a sum could overflow (its first chunk, and a
+        // value 2^64 above): the exponentials of a chunk need not wait for its maximum
+        if ((most - rs.m) * a.c > 64.f) {
+          if (rs.s != 0.f) rs.s *= ds_rescale(rs.m, most, a.c);
+          rs.m = most;
+        }
+        const float m = rs.m == kNegInf ? 0.f : rs.m;   // nothing but -inf (or NaN) so far
+        const bool mwide = ds_wide(m, a.c);
+        rs.s += ds_terms<T, U>(raw, mwide, m, a.c);
+        if (++slot == chunks) {
+          slot = 0;
+          full_parity ^= 1u;
+        }
+      }
+      if (s.edge >= 0 && ze != kNegInf) {
+        const float m = fmaxf(rs.m, ze);
+        rs.s = (rs.m == m ? rs.s : rs.s * ds_rescale(rs.m, m, a.c)) +
+               (ze == m ? 1.f : ex2(ds_exponent(ze, m, a.c)));         // NaN stays NaN
+        rs.m = m;
+      }
+      rs = ds_join_lanes<32>(rs, a.c);
+      mbar_wait(&ready[turn], parity, aborted, err, DEV_ERR_EPI_WAIT);
+      // the list warp has read the row before's statistics: the next message into them can only
+      // follow this row's
+      if (row != blockIdx.y)
+        mbar_wait(&taken[turn ^ 1], turn ? parity : parity ^ 1u, aborted, err, DEV_ERR_EPI_WAIT);
+      if (a.cl > 1) {
+        if (lane < a.cl) ds_send(&stats[turn][part * DS_WARPS + warp], &got[turn], lane, rs);
+      } else if (lane == 0) {
+        stats[turn][warp] = rs;
+        mbar_arrive(&got[turn]);
+      }
+      mbar_wait(&got[turn], parity, aborted, err, DEV_ERR_EPI_WAIT);
+      rs = joined(turn);
+      const float coef = ds_coef(w * a.tau, masses[turn], rs.s);
+      D* dz = static_cast<D*>(a.dz) + row * a.ld_dz;
+      const bool al = store_aligned(s, dz), wide = ds_wide(rs.m, a.c);
+      D* d = dz + s.head + static_cast<int64_t>(s.i0 + tid) * VE;
+      int back = slot0;
+      for (int i = s.i0; i < s.i1; i += DS_CHUNK_VECS, d += DS_CHUNK_VECS * VE) {
+        const uint4* ring = reinterpret_cast<const uint4*>(ds_ring + back * CHUNK) + tid;
+        uint4 raw[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) raw[u] = ring[u * DS_THREADS];
+        put_gradients<T, D, U>(d, DS_THREADS * VE,
+                               (s.i1 - i - tid + DS_THREADS - 1) / DS_THREADS, al, raw, wide, rs.m,
+                               a.c, coef);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[back]);
+        if (++back == chunks) back = 0;
+      }
+      put_edge(s, dz, ze, rs.m, a.c, coef);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&stored[turn]);
+      if (turn) parity ^= 1u;
+      turn ^= 1;
+    }
+  }
+  if (a.cl > 1) {                                     // no CTA ends while a message is under way
+    __syncwarp();
+    ds_cluster_arrive();
+    ds_cluster_wait();
+  }
 }
 
 // Loss and gradient; NV vectors of z per thread stay in registers.
@@ -543,9 +925,12 @@ __global__ void __launch_bounds__(DS_THREADS, NV > 8 ? 2 : (KPT == 1 ? 4 : 3)) d
     raw[n] = i < s.i1 ? s.load(i) : none_vec<T>();
   }
   const float ze = s.edge >= 0 ? ds_ld(z + s.edge) : kNegInf;
+  extern __shared__ int ds_table[];
   Entries<KPT> e;
-  load_entries(a, row, s, part, part == 0, e);
-  clear_table(a);
+  load_entries<DS_THREADS>(a, row, e);
+  gather_logits(s, part, part == 0, e);
+  clear_table<DS_THREADS>(a, ds_table);
+  const float tl = a.top_lse ? a.top_lse[row] : 0.f;
   const float w = a.weight ? a.weight[row] : 1.f;
   RunSum rs{ze, 0.f};
 #pragma unroll
@@ -553,39 +938,43 @@ __global__ void __launch_bounds__(DS_THREADS, NV > 8 ? 2 : (KPT == 1 ? 4 : 3)) d
   // a thread whose entries are all -inf adds nothing, to any reference (NaN it adds)
   const float m = rs.m == kNegInf ? 0.f : rs.m;
   const bool mwide = ds_wide(m, a.c);
-  uint64_t acc = pack2(ex2(ds_exponent(ze, m, a.c)), 0.f);
+  rs.s = ex2(ds_exponent(ze, m, a.c));
 #pragma unroll
-  for (int n = 0; n < NV; ++n) {
-    acc = ds_terms<T>(acc, raw[n], mwide, m, a.c);
-    asm volatile("" : "+l"(acc));                      // one vector unpacked at a time
+  for (int n = 0; n < NV; n += 4) {
+    const uint4 four[4] = {raw[n], raw[n + 1], raw[n + 2], raw[n + 3]};
+    rs.s += ds_terms<T, 4>(four, mwide, m, a.c);
+    asm volatile("" : "+f"(rs.s));                     // four vectors unpacked at a time
   }
-  rs.s = unpack2(acc).x + unpack2(acc).y;
   // the gradient unpacks the vectors again: nothing unpacked lives across the statistics
 #pragma unroll
   for (int n = 0; n < NV; ++n)
     asm volatile("" : "+r"(raw[n].x), "+r"(raw[n].y), "+r"(raw[n].z), "+r"(raw[n].w));
   float mass;
-  row_statistics<true, true, KPT>(a, row, part, w, sh, rs, e, mass);
+  row_statistics<DS_THREADS, true, true, KPT>(
+      a, row, part, w, tl, sh, ds_table, rs, e, mass, [] { __syncthreads(); },
+      [&](RunSum r) { return exchange_cluster(a, sh, r); });
   const float wt = w * a.tau;
   const float coef = ds_coef(wt, mass, rs.s);
   float patch[KPT];
   int patch_id[KPT];
-  list_gradients(a, s, e, rs, coef, wt, part, patch, patch_id);
+  list_gradients<DS_THREADS>(a, sh, s, e, rs, coef, wt, part, ds_table, patch, patch_id);
   D* dz = static_cast<D*>(a.dz) + row * a.ld_dz;
   const bool al = store_aligned(s, dz), wide = ds_wide(rs.m, a.c);
+  const int mine = s.i1 - s.i0 - tid;                   // vectors tid, tid + 256, ... below it
+  D* d = dz + s.head + static_cast<int64_t>(s.i0 + tid) * Vec<T>::VE;
 #pragma unroll
-  for (int n = 0; n < NV; ++n) {
-    const int i = s.i0 + tid + n * DS_THREADS;
-    if (i < s.i1)
-      put_gradients<T, D>(dz + s.head + static_cast<int64_t>(i) * Vec<T>::VE, al, raw[n], wide,
-                          rs.m, a.c, coef);
+  for (int n = 0; n < NV; n += 2) {
+    const uint4 two[2] = {raw[n], raw[n + 1]};
+    put_gradients<T, D, 2>(d + static_cast<int64_t>(n) * DS_THREADS * Vec<T>::VE,
+                           DS_THREADS * Vec<T>::VE,
+                           (mine + DS_THREADS - 1) / DS_THREADS - n, al, two, wide, rs.m, a.c, coef);
   }
   put_edge(s, dz, ze, rs.m, a.c, coef);
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < KPT; ++i)
     if (patch_id[i] >= 0) ds_st(dz + patch_id[i], patch[i]);
-  if (a.cl > 1) ds_cluster_wait();
+  if (a.cl > 1) ds_cluster_wait();                     // a peer may still read this CTA's sums
 }
 
 // LSE: the row's statistics are taken from z (else lse_in). GRAD: dz is written.
@@ -597,9 +986,12 @@ __global__ void __launch_bounds__(DS_THREADS) distill_stream_kernel(DsArgs a) {
   const int tid = threadIdx.x;
   const T* z = static_cast<const T*>(a.z) + row * a.ld_z;
   const Slice<T> s(z, a.v, part, a.per);
+  extern __shared__ int ds_table[];
   Entries<KPT> e;
-  load_entries(a, row, s, part, LSE && part == 0, e);
-  if (GRAD) clear_table(a);
+  load_entries<DS_THREADS>(a, row, e);
+  gather_logits(s, part, LSE && part == 0, e);
+  if (GRAD) clear_table<DS_THREADS>(a, ds_table);
+  const float tl = a.top_lse ? a.top_lse[row] : 0.f;
   const float w = a.weight ? a.weight[row] : 1.f;
   constexpr int U = 4;                               // vectors in flight per thread
   const float ze = s.edge >= 0 ? ds_ld(z + s.edge) : kNegInf;
@@ -620,10 +1012,7 @@ __global__ void __launch_bounds__(DS_THREADS) distill_stream_kernel(DsArgs a) {
       }
       if (!(m > kNegInf)) m = 0.f;                   // nothing but -inf (or NaN) so far
       const bool mwide = ds_wide(m, a.c);
-      uint64_t acc = 0;
-#pragma unroll
-      for (int u = 0; u < U; ++u) acc = ds_terms<T>(acc, raw[u], mwide, m, a.c);
-      rs.s += unpack2(acc).x + unpack2(acc).y;
+      rs.s += ds_terms<T, U>(raw, mwide, m, a.c);
     }
   } else {
     // q = 2^(z c - fl(m c)) / s with m = lse tau rounded to fp32, s = what the roundings left
@@ -636,13 +1025,15 @@ __global__ void __launch_bounds__(DS_THREADS) distill_stream_kernel(DsArgs a) {
     rs.s = l == kNegInf ? 0.f : expf(static_cast<float>(left));
   }
   float mass;
-  row_statistics<LSE, GRAD, KPT>(a, row, part, w, sh, rs, e, mass);
+  row_statistics<DS_THREADS, LSE, GRAD, KPT>(
+      a, row, part, w, tl, sh, ds_table, rs, e, mass, [] { __syncthreads(); },
+      [&](RunSum r) { return exchange_cluster(a, sh, r); });
   if (GRAD) {
     const float wt = w * a.tau;
     const float coef = ds_coef(wt, mass, rs.s);
     float patch[KPT];
     int patch_id[KPT];
-    list_gradients(a, s, e, rs, coef, wt, part, patch, patch_id);
+    list_gradients<DS_THREADS>(a, sh, s, e, rs, coef, wt, part, ds_table, patch, patch_id);
     D* dz = static_cast<D*>(a.dz) + row * a.ld_dz;
     const bool al = store_aligned(s, dz), wide = ds_wide(rs.m, a.c);
     // dz may be z: every entry's z[id] was read before the first barrier above
@@ -651,11 +1042,9 @@ __global__ void __launch_bounds__(DS_THREADS) distill_stream_kernel(DsArgs a) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (i + u * DS_THREADS < s.i1) raw[u] = s.load(i + u * DS_THREADS);
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (i + u * DS_THREADS < s.i1)
-          put_gradients<T, D>(dz + s.head + static_cast<int64_t>(i + u * DS_THREADS) * Vec<T>::VE,
-                              al, raw[u], wide, rs.m, a.c, coef);
+      put_gradients<T, D, U>(dz + s.head + static_cast<int64_t>(i) * Vec<T>::VE,
+                             DS_THREADS * Vec<T>::VE, (s.i1 - i + DS_THREADS - 1) / DS_THREADS, al,
+                             raw, wide, rs.m, a.c, coef);
     }
     put_edge(s, dz, ze, rs.m, a.c, coef);
     __syncthreads();
@@ -663,30 +1052,81 @@ __global__ void __launch_bounds__(DS_THREADS) distill_stream_kernel(DsArgs a) {
     for (int i = 0; i < KPT; ++i)
       if (patch_id[i] >= 0) ds_st(dz + patch_id[i], patch[i]);
   }
-  if (LSE && a.cl > 1) ds_cluster_wait();
+  if (LSE && a.cl > 1) ds_cluster_wait();              // a peer may still read this CTA's sums
+}
+
+cudaLaunchConfig_t ds_config(const DsArgs& a, int64_t rows, int threads, size_t smem, bool cluster,
+                             cudaLaunchAttribute* attr, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.cl, static_cast<unsigned>(rows));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = static_cast<unsigned>(a.cl);
+  attr->val.clusterDim.y = 1;
+  attr->val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster && a.cl > 1 ? 1 : 0;
+  return cfg;
 }
 
 kronq_status launch_rows(void (*kern)(DsArgs), DsArgs a, int n, bool cluster, bool table,
                          const char* what, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(DS_THREADS);
-  cfg.dynamicSmemBytes = table ? id_table_bytes(a) : 0;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(a.cl);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster && a.cl > 1 ? 1 : 0;
   constexpr int most = 65535;                      // rows per launch: the grid's y extent
+  const size_t smem = table ? 4 * static_cast<size_t>(id_table_words(a)) : 0;
   for (a.row0 = 0; a.row0 < n; a.row0 += most) {
-    cfg.gridDim = dim3(a.cl, static_cast<unsigned>(std::min<int64_t>(most, n - a.row0)));
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = ds_config(a, std::min<int64_t>(most, n - a.row0), DS_THREADS,
+                                             smem, cluster, &attr, stream);
     const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, a);
     if (err != cudaSuccess) return fail(KRONQ_ERR_CUDA, "%s: %s", what, cudaGetErrorString(err));
     KQ_TRY(check_launch(what));
   }
   return KRONQ_OK;
+}
+
+// Shared memory of the ring kernel: the chunks, then for each list warp the id table and the
+// entries' logits, z, ids and gradients. Two CTAs per SM where a row fits them.
+size_t ring_list_bytes(const DsArgs& a) {
+  return 8 * (static_cast<size_t>(id_table_words(a)) + 4 * a.k);
+}
+int ring_chunks(const DsArgs& a, int ctas) {
+  const int64_t room = (ctas == 2 ? 111 : 224) * 1024 - static_cast<int64_t>(ring_list_bytes(a));
+  return static_cast<int>(std::min<int64_t>(DS_MAX_CHUNKS, room / (DS_CHUNK_VECS * 16)));
+}
+
+template <typename T, typename D>
+kronq_status launch_ring(const DsArgs& a, int n, int ctas, cudaStream_t stream) {
+  const int chunks = ring_chunks(a, ctas);
+  const size_t smem = static_cast<size_t>(chunks) * DS_CHUNK_VECS * 16 + ring_list_bytes(a);
+  auto kern = distill_ring_kernel<T, D>;
+  KQ_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   static_cast<int>(smem)));
+  int* err = device_error_word();
+  if (!err) return fail(KRONQ_ERR_CUDA, "device error word unavailable");
+  // As many clusters as run at once: one more would start when all others have ended. The query
+  // takes about 15 us, so its last answer is kept (it depends on the device, cl and smem).
+  cudaLaunchAttribute attr;
+  cudaLaunchConfig_t cfg = ds_config(a, 1, DS_RING_THREADS, smem, true, &attr, stream);
+  int clusters = ctas * device_sms();
+  if (a.cl > 1) {
+    static thread_local int64_t key = -1;
+    static thread_local int answer = 0;
+    int dev = 0;
+    KQ_CUDA_TRY(cudaGetDevice(&dev));
+    const int64_t k = (static_cast<int64_t>(dev) << 32) + (static_cast<int64_t>(a.cl) << 24) + smem;
+    if (k != key) {
+      KQ_CUDA_TRY(cudaOccupancyMaxActiveClusters(&answer, kern, &cfg));
+      key = k;
+    }
+    clusters = answer;
+  }
+  cfg.gridDim.y = static_cast<unsigned>(std::min(n, std::max(1, clusters)));
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, static_cast<int64_t>(n), chunks, err);
+  if (e != cudaSuccess)
+    return fail(KRONQ_ERR_CUDA, "distill_ring_kernel: %s", cudaGetErrorString(e));
+  return check_launch("distill_ring_kernel");
 }
 
 template <typename T, typename D, int KPT>
@@ -701,13 +1141,26 @@ kronq_status launch_distill(DsArgs a, int n, bool lse, bool grad, cudaStream_t s
     return launch_rows(distill_stream_kernel<T, D, false, true, KPT>, a, n, false, true,
                        "distill_stream_kernel", stream);
   }
+  auto cut = [&] { return static_cast<int>((vecs + a.cl - 1) / a.cl); };
+  if (grad) {
+    // Long rows, at least two per cluster: the fewest CTAs that hold a row with two chunks to spare
+    for (int ctas = 2; ctas >= 1 && vecs > DS_RING_MIN_VECS; --ctas) {
+      const int hold = ring_chunks(a, ctas) - 2;
+      a.cl = 1;
+      while (a.cl < DS_MAX_CL && vecs > static_cast<int64_t>(a.cl) * hold * DS_CHUNK_VECS)
+        a.cl *= 2;
+      a.per = cut();
+      if (a.per <= hold * DS_CHUNK_VECS &&
+          static_cast<int64_t>(n) * a.cl >= 2 * ctas * device_sms())
+        return launch_ring<T, D>(a, n, ctas, stream);
+    }
+  }
   // Slices: enough to give every SM two CTAs when rows are few, none shorter than one vector per
   // thread.
   a.cl = 1;
   while (a.cl < DS_MAX_CL && static_cast<int64_t>(n) * a.cl < 2 * device_sms() &&
          vecs > static_cast<int64_t>(a.cl) * DS_THREADS)
     a.cl *= 2;
-  auto cut = [&] { return static_cast<int>((vecs + a.cl - 1) / a.cl); };
   a.per = cut();
   if (!grad)
     return launch_rows(distill_stream_kernel<T, D, true, false, KPT>, a, n, true, false,
@@ -716,14 +1169,15 @@ kronq_status launch_distill(DsArgs a, int n, bool lse, bool grad, cudaStream_t s
   a.per = cut();
   auto kern = a.per <= DS_THREADS * NV       ? distill_hold_kernel<T, D, NV, KPT>
               : a.per <= DS_THREADS * 2 * NV ? distill_hold_kernel<T, D, 2 * NV, KPT>
-                                           : distill_stream_kernel<T, D, true, true, KPT>;
+                                             : distill_stream_kernel<T, D, true, true, KPT>;
   return launch_rows(kern, a, n, true, true, "distill kernel", stream);
 }
 
 template <typename T, typename D>
 kronq_status launch_distill(const DsArgs& a, int n, bool lse, bool grad, cudaStream_t stream) {
-  return a.k <= DS_THREADS ? launch_distill<T, D, 1>(a, n, lse, grad, stream)
-                           : launch_distill<T, D, DS_KPT_MAX>(a, n, lse, grad, stream);
+  return a.k <= DS_THREADS
+             ? launch_distill<T, D, 1>(a, n, lse, grad, stream)
+             : launch_distill<T, D, kMaxDistillTop / DS_THREADS>(a, n, lse, grad, stream);
 }
 
 }  // namespace

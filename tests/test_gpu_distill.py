@@ -280,3 +280,51 @@ def test_the_head_gradient_feeds_the_statistics(K):
     want = g.T @ g
     # each factor is a bf16 rounding (2^-8) off: twice that in a product, in the norm
     assert np.linalg.norm(np64(hg) - want) <= 2.0 * 2.0 ** -8 * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("v,k,dtype", [(128256, 128, torch.bfloat16), (40001, 300, torch.bfloat16),
+                                       (70000, 7, torch.float32), (300000, 64, torch.bfloat16),
+                                       (20000, 1024, torch.float32)])
+def test_many_long_rows(K, v, k, dtype):
+    """Enough rows that every CTA takes several in turn; each row against fp64 on the device."""
+    n, tau = 1400, 1.3
+    g = torch.Generator(device="cuda")
+    g.manual_seed(v)
+    z = torch.empty(n, v, dtype=dtype, device="cuda")
+    for r in range(0, n, 200):
+        z[r:r + 200] = 2.0 * torch.randn(200, v, generator=g, device="cuda")
+    start = torch.randint(0, v, (n, 1), generator=g, device="cuda")
+    ids = ((start + torch.arange(k, device="cuda") * (v // k - 1)) % v).to(torch.int32)
+    ids[5::9, k // 2:] = -1
+    if k > 2:
+        ids[7::11, 2] = ids[7::11, 0]                  # listed twice
+    t = (9.0 - torch.arange(k, device="cuda") / k * 4).expand(n, k).to(dtype).contiguous()
+    z.scatter_(1, ids.clamp(min=0).long(), t)
+    w = torch.rand(n, generator=g, device="cuda")
+    first = None
+    for _ in range(3):
+        loss, lse, dz = run(K, z, ids, t, tau, None, w)
+        if first is None:
+            first = (loss, lse, dz)
+        else:
+            assert all(torch.equal(a, b) for a, b in zip(first, (loss, lse, dz)))
+    stat = (v / 256 + 64) * 2.0 ** -23
+    for r in range(0, n, 50):
+        rows = slice(r, r + 50)
+        u = z[rows].double() / tau
+        l = torch.logsumexp(u, 1)
+        there = ids[rows] >= 0
+        at = ids[rows].clamp(min=0).long()
+        logp = torch.log_softmax((t[rows].double() / tau).masked_fill(~there, -math.inf), 1)
+        p = logp.exp()
+        wl = w[rows].double() * tau * tau * (p * (logp - u.gather(1, at) + l[:, None])).masked_fill(
+            ~there, 0.0).sum(1)
+        q = (u - l[:, None]).exp()
+        unit = w[rows].double()[:, None] * tau
+        wg = unit * (q - torch.zeros_like(q).scatter_add_(1, at, p))
+        assert bool(((lse[rows].double() - l).abs() <= stat + 2 * U32 * l.abs()).all())
+        assert bool(((loss[rows].double() - wl).abs() <= tau * tau * (stat + 4e3 * U32)
+                     + 2 * U32 * wl.abs()).all())
+        tol = (stat + 6 * 40 * U32) * (2 * unit * q + wg.abs()) + HALF[dtype] * wg.abs() + 1e-38
+        assert bool(((dz[rows].double() - wg).abs() <= tol).all())
+    assert K.kronq_device_error() == 0
