@@ -18,8 +18,9 @@ namespace {
 
 constexpr int MM_BM = 128;        // channels per tile (MMA M)
 constexpr int MM_BK = 128;        // K bytes per pipeline stage (one 128-byte swizzled row)
-constexpr int MM_THREADS = 192;   // TMA producer, MMA issuer, 4 epilogue warps
-constexpr int MM_GROUP = 16;      // channel tiles visited together (operand reuse in L2)
+constexpr int MM_THREADS = 192;   // pair kernel: TMA producer, MMA issuer, 4 epilogue warps
+constexpr int SP_THREADS = 256;   // split kernel: warps 0 and 1 produce and issue, all 8 finish
+constexpr int MM_GROUP = 8;       // channel tiles visited together (operand reuse in L2)
 
 struct MmParams {
   const float* tok_scale;
@@ -102,30 +103,37 @@ __device__ __forceinline__ __nv_bfloat16 mm_out<__nv_bfloat16>(float v) {
   return __float2bfloat16_rn(v);
 }
 
-// One output from its exact sum; sum_t and s_t are the token's. One fp32 product of the scales
-// and one with the (exactly formed, once rounded) sum.
+// One output from its exact sum.
 __device__ __forceinline__ float mm_value(const Channel& c, int acc, float s_t, int sum_t) {
-  float f;
-  if (c.wide)
-    f = static_cast<float>(static_cast<double>(acc) -
-                           static_cast<double>(c.z) * static_cast<double>(sum_t));
-  else
-    f = static_cast<float>(static_cast<int>(static_cast<uint32_t>(acc) -
-                                            static_cast<uint32_t>(c.zi) *
-                                                static_cast<uint32_t>(sum_t)));
+  const float f =
+      c.wide ? static_cast<float>(static_cast<double>(acc) -
+                                  static_cast<double>(c.z) * static_cast<double>(sum_t))
+             : static_cast<float>(static_cast<int>(static_cast<uint32_t>(acc) -
+                                                   static_cast<uint32_t>(c.zi) *
+                                                       static_cast<uint32_t>(sum_t)));
   return f * (c.s * s_t);
 }
 
-template <int BN>
-struct MmCfg {
-  static constexpr int A_BYTES = MM_BM * MM_BK;
-  static constexpr int B_BYTES = BN * MM_BK;
-  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int STAGES = BN >= 256 ? 4 : 6;
-  static constexpr int TOK_BYTES = 4 * BN * 8;              // (s_t, sum_t) pairs per epilogue warp
-  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + TOK_BYTES + 1024 + 256;
-  static constexpr int TMEM_COLS = 2 * BN < 32 ? 32 : 2 * BN;
-};
+// 16 outputs of a channel from their exact sums and the tokens' (s_t, sum_t): one fp32 product of
+// the scales and one with the (exactly formed, once rounded) sum.
+__device__ __forceinline__ void mm_values(const Channel& c, bool any_wide, const uint32_t (&acc)[16],
+                                          const float2 (&tok)[16], float (&out)[16]) {
+  if (any_wide && c.wide) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      out[j] = static_cast<float>(static_cast<double>(static_cast<int>(acc[j])) -
+                                  static_cast<double>(c.z) *
+                                      static_cast<double>(__float_as_int(tok[j].y))) *
+               (c.s * tok[j].x);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      out[j] = static_cast<float>(static_cast<int>(
+                   acc[j] - static_cast<uint32_t>(c.zi) *
+                                static_cast<uint32_t>(__float_as_int(tok[j].y)))) *
+               (c.s * tok[j].x);
+  }
+}
 
 __device__ __forceinline__ void mm_tile(const MmParams& p, int t, int& tm, int& tn) {
   const int per_group = MM_GROUP * p.tiles_n;
@@ -135,34 +143,110 @@ __device__ __forceinline__ void mm_tile(const MmParams& p, int t, int& tm, int& 
   tn = r / rows;
 }
 
+// One epilogue warp's part of a tile: 32 channels (lane = channel) by `cols` tokens from t0. All 16
+// outputs of a step are formed before any is stored: a store would hold back the loads behind it.
+template <typename Y>
+__device__ __forceinline__ void store_tile(const MmParams& p, const Channel& c, const float2* tok,
+                                           uint32_t taddr, int t0, int cols, int ch) {
+  Y* yp = static_cast<Y*>(p.y) + static_cast<int64_t>(t0) * p.ld_y + ch;
+  const bool any_wide = __any_sync(0xffffffffu, c.wide);
+  const bool in = ch < p.d_out;
+  for (int cb = 0; cb < cols; cb += 16, yp += 16 * p.ld_y) {
+    uint32_t v[16];
+    float2 ts[16];
+    float out[16];
+    mm_tmem_ld_x16(taddr + cb, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float4 two = reinterpret_cast<const float4*>(tok + cb)[j];
+      ts[2 * j] = make_float2(two.x, two.y);
+      ts[2 * j + 1] = make_float2(two.z, two.w);
+    }
+    tmem_ld_wait();
+    mm_values(c, any_wide, v, ts, out);
+    if (in) {
+      if (cb + 16 <= cols) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) yp[j * p.ld_y] = mm_out<Y>(out[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (cb + j < cols) yp[j * p.ld_y] = mm_out<Y>(out[j]);
+      }
+    }
+  }
+}
+
+kronq_status byte_map(CUtensorMap* map, const void* base, int64_t ld, int cols, int64_t rows,
+                      uint32_t box_rows) {
+  const uint64_t dims[2] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows)};
+  const uint64_t strides[1] = {static_cast<uint64_t>(ld)};
+  const uint32_t box[2] = {MM_BK, box_rows};
+  return encode_tiled_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box,
+                          CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// ---------------------------------------------------------------------------------------------
+// Few tokens, or few tiles: K split over a cluster
+// ---------------------------------------------------------------------------------------------
+// A tile is 128 channels by BN (16 .. 128) tokens; the cl CTAs of a cluster take consecutive parts
+// of K, so that a matrix with few channel tiles still has enough CTAs to stream it (two per SM,
+// about 90 KB in flight each). Their int32 sums meet in distributed shared memory: the CTAs share
+// the tile's outputs out among their threads, each of which adds the cl sums of an output. Integer
+// sums: the split changes no bit. A tcgen05 MMA of up to 128 columns takes 63 cycles for 4 KB of
+// codes (measured), three times the rate at which HBM delivers them. A thread keeps one channel,
+// whose grid it loads before the codes arrive.
+template <int BN>
+struct MmCfg {
+  static constexpr int A_BYTES = MM_BM * MM_BK;
+  static constexpr int B_BYTES = BN * MM_BK;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int STAGES = BN <= 32 ? 5 : BN == 64 ? 4 : 3;
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + BN * 8 + 1024 + 128;
+  static constexpr int TMEM_COLS = BN < 32 ? 32 : BN;
+  static_assert(STAGES * STAGE_BYTES >= BN * MM_BM * 4, "the sums reuse the ring");
+};
+
+__device__ __forceinline__ uint32_t mm_map(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void mm_cluster_sync() {
+  asm volatile(
+      "barrier.cluster.arrive.release.aligned;\n\t"
+      "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// grid: x = K part (the cluster), y = channel tile, z = token tile
 template <int BN, typename Y>
-__global__ void __launch_bounds__(MM_THREADS, 1)
-    i8matmul_kernel(const __grid_constant__ CUtensorMap tma_w,
-                    const __grid_constant__ CUtensorMap tma_q, const MmParams p) {
+__global__ void __launch_bounds__(SP_THREADS, 2)
+    i8matmul_split_kernel(const __grid_constant__ CUtensorMap tma_w,
+                          const __grid_constant__ CUtensorMap tma_q, const MmParams p) {
   using C = MmCfg<BN>;
   constexpr int STAGES = C::STAGES;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  float2* tok_all = reinterpret_cast<float2*>(smem + STAGES * C::STAGE_BYTES);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * C::STAGE_BYTES + C::TOK_BYTES);
+  int* sums = reinterpret_cast<int*>(smem);          // [token][channel], once the ring is done
+  float2* tok = reinterpret_cast<float2*>(smem + STAGES * C::STAGE_BYTES);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * C::STAGE_BYTES + BN * 8);
   uint64_t* empty = full + STAGES;
-  uint64_t* tfull = empty + STAGES;
-  uint64_t* tempty = tfull + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
+  uint64_t* done = empty + STAGES;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int num_tiles = p.tiles_m * p.tiles_n;
+  const int cl = gridDim.x, rank = blockIdx.x;
+  const int tm = blockIdx.y, tn = blockIdx.z;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(p.kblocks) * rank / cl);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(p.kblocks) * (rank + 1) / cl);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int a = 0; a < 2; ++a) {
-      mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], 4);
-    }
+    mbar_init(done, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -178,13 +262,221 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  const int cols = min(BN, p.n - tn * BN);
+  const int ch = tm * MM_BM + (threadIdx.x & (MM_BM - 1));    // this thread's channel
+  Channel c{};
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      int it = 0;
+      for (; it < kb1 - kb0; ++it) {
+        const int s = it % STAGES;
+        const uint32_t ph = (it / STAGES) & 1u;
+        if (!mbar_wait(&empty[s], ph ^ 1u, abort_flag, p.err, DEV_ERR_TMA_WAIT)) break;
+        uint8_t* st = smem + s * C::STAGE_BYTES;
+        mbar_arrive_expect_tx(&full[s], C::STAGE_BYTES);
+        tma_load_2d(st, &tma_w, &full[s], (kb0 + it) * MM_BK, tm * MM_BM);
+        tma_load_2d(st + C::A_BYTES, &tma_q, &full[s], (kb0 + it) * MM_BK, tn * BN);
+      }
+      if (it < kb1 - kb0)
+        for (int j = max(0, it - STAGES); j < it; ++j)
+          mbar_drain(&full[j % STAGES], (j / STAGES) & 1u, 1000000000ull);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      const uint32_t idesc = mm_idesc(MM_BM, BN, p.is_signed != 0);
+      for (int it = 0; it < kb1 - kb0; ++it) {
+        const int s = it % STAGES;
+        if (!mbar_wait(&full[s], (it / STAGES) & 1u, abort_flag, p.err, DEV_ERR_MMA_WAIT)) break;
+        tc_fence_after();
+        const uint32_t base = smem_u32(smem + s * C::STAGE_BYTES);
+#pragma unroll
+        for (int kk = 0; kk < MM_BK / 32; ++kk)
+          umma_i8(tmem_base, smem_desc_sw128(base + kk * 32, 16, 1024),
+                  smem_desc_sw128(base + C::A_BYTES + kk * 32, 16, 1024), idesc,
+                  (it == 0 && kk == 0) ? 0u : 1u);
+        umma_commit(&empty[s]);
+      }
+      umma_commit(done);
+    }
+  }
+  if (warp >= 2)
+    for (int j = threadIdx.x - 64; j < cols; j += SP_THREADS - 64)
+      tok[j] = make_float2(p.tok_scale[tn * BN + j],
+                           __int_as_float(p.tok_sum ? p.tok_sum[tn * BN + j] : 0));
+  c = load_channel(p, ch);
+  __syncwarp();
+  const bool ok = mbar_wait(done, 0, abort_flag, p.err, DEV_ERR_EPI_WAIT);
+  __syncthreads();     // every role has left its loop; the MMAs and the copies they used are done
+  tc_fence_after();
+  const int q = warp & 3, half = warp >> 2;
+  const uint32_t taddr = tmem_base + ((q * 32u) << 16);
+  if (cl == 1) {
+    // columns 32 k + 16 half .. + 15: two warps per 32 channels
+    if (ok)
+      for (int cb = 16 * half; cb < cols; cb += 32)
+        store_tile<Y>(p, c, tok + cb, taddr + cb, tn * BN + cb, min(16, cols - cb), ch);
+  } else {
+    if (ok)
+      for (int cb = 16 * half; cb < cols; cb += 32) {
+        uint32_t v[16];
+        mm_tmem_ld_x16(taddr + cb, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) sums[(cb + j) * MM_BM + q * 32 + lane] = static_cast<int>(v[j]);
+      }
+    mm_cluster_sync();
+    Y* y = static_cast<Y*>(p.y) + static_cast<int64_t>(tn) * BN * p.ld_y + ch;
+    // token t of the tile belongs to CTA (t / 2) mod cl, its half t mod 2 of the threads; the
+    // remote reads of four tokens are under way together
+    uint32_t peer[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+      peer[r] = mm_map(sums + q * 32 + lane, r < cl ? r : 0);
+    constexpr int U = 4;
+    for (int t0 = 2 * rank + half; t0 < cols; t0 += U * 2 * cl) {
+      int part[U][8];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          part[u][r] = 0;
+          const int t = t0 + u * 2 * cl;
+          if (r < cl && t < cols)
+            asm volatile("ld.shared::cluster.s32 %0, [%1];"
+                         : "=r"(part[u][r])
+                         : "r"(peer[r] + t * (MM_BM * 4))
+                         : "memory");
+        }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int t = t0 + u * 2 * cl;
+        if (t < cols && ch < p.d_out) {
+          int acc = 0;
+#pragma unroll
+          for (int r = 0; r < 8; ++r) acc += part[u][r];
+          y[t * p.ld_y] = mm_out<Y>(mm_value(c, acc, tok[t].x, __float_as_int(tok[t].y)));
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  if (cl > 1)
+    mm_cluster_sync();                               // no CTA ends while a peer reads its sums
+  else
+    __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem_base, C::TMEM_COLS);
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// Prompts: two SMs on one tile
+// ---------------------------------------------------------------------------------------------
+// A pair of CTAs multiplies 256 channels by 256 tokens (tcgen05 cta_group::2, M = 256): each CTA
+// holds its 128 channels and half of the tokens, so an operand byte from L2 feeds 1.5 times the
+// tensor work of a 128 x 256 tile of one CTA (32 KB per CTA and 128 columns of K instead of 48).
+// The even CTA of the pair issues the MMAs; each CTA's producer fills its own shared memory and
+// counts the bytes on the even CTA's barrier; accumulators are double-buffered in tensor memory
+// (2 x 256 columns), each CTA drains its own 128 channels.
+namespace pr {
+constexpr int BN = 256;
+constexpr int A_BYTES = 128 * MM_BK, B_BYTES = 128 * MM_BK;
+constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int STAGES = 6;
+constexpr int TOK_BYTES = 4 * BN * 8;
+constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + TOK_BYTES + 1024 + 256;
+constexpr int TMEM_COLS = 512;
+}  // namespace pr
+
+// 2-D tiled TMA load into this CTA's shared memory, completion counted on a barrier of the pair.
+__device__ __forceinline__ void pr_load(void* dst, const CUtensorMap* map, uint32_t bar, int32_t x,
+                                        int32_t y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void pr_mma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrive once on `bar` of both CTAs when this thread's MMAs so far have completed.
+__device__ __forceinline__ void pr_commit(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;" ::"r"(smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+__device__ __forceinline__ void pr_arrive_remote(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+template <typename Y>
+__global__ void __launch_bounds__(MM_THREADS, 1)
+    i8matmul_pair_kernel(const __grid_constant__ CUtensorMap tma_w,
+                         const __grid_constant__ CUtensorMap tma_q, const MmParams p) {
+  using namespace pr;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  float2* tok_all = reinterpret_cast<float2*>(smem + STAGES * STAGE_BYTES);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE_BYTES + TOK_BYTES);
+  uint64_t* empty = full + STAGES;
+  uint64_t* tfull = empty + STAGES;
+  uint64_t* tempty = tfull + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = blockIdx.x & 1;                   // the cluster is (2, 1, 1)
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int num_tiles = p.tiles_m * p.tiles_n;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], 8);                      // four epilogue warps of each CTA
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tensormap(&tma_w);
+    prefetch_tensormap(&tma_q);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_slot)),
+                 "r"(TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  mm_cluster_sync();                                 // the peer's barriers exist
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
 
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer
     if (lane == 0) {
       uint32_t it = 0;
       bool ok = true;
-      for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
+      for (int t = pair; t < num_tiles && ok; t += pairs) {
         int tm, tn;
         mm_tile(p, t, tm, tn);
         for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
@@ -194,24 +486,28 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
             ok = false;
             break;
           }
-          uint8_t* st = smem + s * C::STAGE_BYTES;
-          mbar_arrive_expect_tx(&full[s], C::STAGE_BYTES);
-          tma_load_2d(st, &tma_w, &full[s], kb * MM_BK, tm * MM_BM);
-          tma_load_2d(st + C::A_BYTES, &tma_q, &full[s], kb * MM_BK, tn * BN);
+          uint8_t* st = smem + s * STAGE_BYTES;
+          // the even CTA's barrier counts both CTAs' bytes (a peer's copy may come before this)
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * STAGE_BYTES);
+          const uint32_t bar = mm_map(&full[s], 0);
+          pr_load(st, &tma_w, bar, kb * MM_BK, tm * 256 + rank * 128);
+          pr_load(st + A_BYTES, &tma_q, bar, kb * MM_BK, tn * BN + rank * 128);
         }
       }
+      // after a wait that gave up, the copies in flight land before the CTA ends (both CTAs count on
+      // the even one's barriers, which the odd one cannot wait for: it waits out the time)
       if (!ok) {
         for (uint32_t j = it > STAGES ? it - STAGES : 0; j < it; ++j)
-          mbar_drain(&full[j % STAGES], (j / STAGES) & 1u, 1000000000ull);
+          mbar_drain(&full[j % STAGES], (j / STAGES) & 1u, 100000000ull);
       }
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      const uint32_t idesc = mm_idesc(MM_BM, BN, p.is_signed != 0);
+    // ------------------------------------------------------------------ MMA issuer (even CTA)
+    if (lane == 0 && rank == 0) {
+      const uint32_t idesc = mm_idesc(256, BN, p.is_signed != 0);
       uint32_t it = 0, ui = 0;
       bool ok = true;
-      for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x, ++ui) {
+      for (int t = pair; t < num_tiles && ok; t += pairs, ++ui) {
         const uint32_t a = ui & 1u, aph = (ui >> 1) & 1u;
         if (!mbar_wait(&tempty[a], aph ^ 1u, abort_flag, p.err, DEV_ERR_MMA_WAIT)) break;
         tc_fence_after();
@@ -224,16 +520,16 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t base = smem_u32(smem + s * C::STAGE_BYTES);
+          const uint32_t base = smem_u32(smem + s * STAGE_BYTES);
 #pragma unroll
           for (int kk = 0; kk < MM_BK / 32; ++kk)
-            umma_i8(d_tmem, smem_desc_sw128(base + kk * 32, 16, 1024),
-                    smem_desc_sw128(base + C::A_BYTES + kk * 32, 16, 1024), idesc,
-                    (kb == 0 && kk == 0) ? 0u : 1u);
-          umma_commit(&empty[s]);
+            pr_mma(d_tmem, smem_desc_sw128(base + kk * 32, 16, 1024),
+                   smem_desc_sw128(base + A_BYTES + kk * 32, 16, 1024), idesc,
+                   (kb == 0 && kk == 0) ? 0u : 1u);
+          pr_commit(&empty[s]);
         }
         if (!ok) break;
-        umma_commit(&tfull[a]);
+        pr_commit(&tfull[a]);
       }
     }
   } else {
@@ -241,11 +537,11 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
     const int q = warp & 3;
     float2* tok = tok_all + q * BN;
     uint32_t ui = 0;
-    for (int t = blockIdx.x; t < num_tiles; t += gridDim.x, ++ui) {
+    for (int t = pair; t < num_tiles; t += pairs, ++ui) {
       int tm, tn;
       mm_tile(p, t, tm, tn);
       const uint32_t a = ui & 1u, aph = (ui >> 1) & 1u;
-      const int ch = tm * MM_BM + q * 32 + lane;
+      const int ch = tm * 256 + rank * 128 + q * 32 + lane;
       const int t0 = tn * BN, cols = min(BN, p.n - t0);
       const Channel c = load_channel(p, ch);
       for (int j = lane; j < cols; j += 32)
@@ -256,68 +552,119 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t taddr = tmem_base + ((q * 32u) << 16) + a * BN;
-      Y* yp = static_cast<Y*>(p.y) + static_cast<int64_t>(t0) * p.ld_y + ch;
-      for (int cb = 0; cb < cols; cb += 16) {
-        uint32_t v[16];
-        mm_tmem_ld_x16(taddr + cb, v);
-        tmem_ld_wait();
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          if (cb + j < cols && ch < p.d_out) {
-            const float2 ts = tok[cb + j];
-            yp[static_cast<int64_t>(cb + j) * p.ld_y] =
-                mm_out<Y>(mm_value(c, static_cast<int>(v[j]), ts.x, __float_as_int(ts.y)));
-          }
-        }
-      }
+      store_tile<Y>(p, c, tok, tmem_base + ((q * 32u) << 16) + a * BN, t0, cols, ch);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&tempty[a]);
+      if (lane == 0) pr_arrive_remote(mm_map(&tempty[a], 0));
     }
   }
 
   tc_fence_before();
   __syncthreads();
+  mm_cluster_sync();       // no MMA, copy or arrival of the pair is under way any more
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem_base, C::TMEM_COLS);
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
+                 "r"(TMEM_COLS)
+                 : "memory");
   }
 }
 
-template <int BN, typename Y>
-kronq_status launch_mm(const I8MatmulArgs& a, MmParams p, cudaStream_t stream) {
-  using C = MmCfg<BN>;
-  p.tiles_m = (a.d_out + MM_BM - 1) / MM_BM;
-  p.tiles_n = (a.n + BN - 1) / BN;
+template <typename Y>
+kronq_status launch_pair(const I8MatmulArgs& a, MmParams p, cudaStream_t stream) {
+  p.tiles_m = (a.d_out + 255) / 256;
+  p.tiles_n = (a.n + pr::BN - 1) / pr::BN;
   CUtensorMap mw, mq;
-  const uint64_t wd[2] = {static_cast<uint64_t>(a.d_in), static_cast<uint64_t>(a.d_out)};
-  const uint64_t ws[1] = {static_cast<uint64_t>(a.ld_codes)};
-  const uint32_t wb[2] = {MM_BK, MM_BM};
-  KQ_TRY(encode_tiled_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.codes, wd, ws, wb,
-                          CU_TENSOR_MAP_SWIZZLE_128B));
-  const uint64_t qd[2] = {static_cast<uint64_t>(a.d_in), static_cast<uint64_t>(a.n)};
-  const uint64_t qs[1] = {static_cast<uint64_t>(a.ld_q)};
-  const uint32_t qb[2] = {MM_BK, BN};
-  KQ_TRY(encode_tiled_map(&mq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.q, qd, qs, qb,
-                          CU_TENSOR_MAP_SWIZZLE_128B));
-  auto kern = i8matmul_kernel<BN, Y>;
+  KQ_TRY(byte_map(&mw, a.codes, a.ld_codes, a.d_in, a.d_out, 128));
+  KQ_TRY(byte_map(&mq, a.q, a.ld_q, a.d_in, a.n, 128));
+  auto kern = i8matmul_pair_kernel<Y>;
   KQ_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   C::SMEM_BYTES));
+                                   pr::SMEM_BYTES));
   const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
-  const int grid = static_cast<int>(std::min<int64_t>(tiles, sm_budget()));
-  kern<<<grid, MM_THREADS, C::SMEM_BYTES, stream>>>(mw, mq, p);
-  return check_launch("i8matmul_kernel");
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min<int64_t>(tiles, std::max(1, sm_budget() / 2))));
+  cfg.blockDim = dim3(MM_THREADS);
+  cfg.dynamicSmemBytes = pr::SMEM_BYTES;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 2;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mw, mq, p);
+  if (e != cudaSuccess)
+    return fail(KRONQ_ERR_CUDA, "i8matmul_pair_kernel: %s", cudaGetErrorString(e));
+  return check_launch("i8matmul_pair_kernel");
 }
 
+template <int BN, typename Y>
+kronq_status launch_split(const I8MatmulArgs& a, const MmParams& p, int cl, cudaStream_t stream) {
+  using C = MmCfg<BN>;
+  CUtensorMap mw, mq;
+  KQ_TRY(byte_map(&mw, a.codes, a.ld_codes, a.d_in, a.d_out, MM_BM));
+  KQ_TRY(byte_map(&mq, a.q, a.ld_q, a.d_in, a.n, BN));
+  auto kern = i8matmul_split_kernel<BN, Y>;
+  KQ_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   C::SMEM_BYTES));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(cl, (a.d_out + MM_BM - 1) / MM_BM, (a.n + BN - 1) / BN);
+  cfg.blockDim = dim3(SP_THREADS);
+  cfg.dynamicSmemBytes = C::SMEM_BYTES;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(cl);
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = cl > 1 ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mw, mq, p);
+  if (e != cudaSuccess)
+    return fail(KRONQ_ERR_CUDA, "i8matmul_split_kernel: %s", cudaGetErrorString(e));
+  return check_launch("i8matmul_split_kernel");
+}
+
+// Which kernel, and into how many parts K is cut: by estimated nanoseconds, from measurements on one
+// B200 (K blocks of 128 columns; a launch's own 4 us left out). A split CTA takes 260 a K block for
+// up to 64 tokens, 300 when two share an SM, 360 and 440 for 128 tokens; joining the sums takes
+// about 90 a token and CTA of the cluster, a further wave of CTAs 2500; a pair tile 370 a K block.
+// Measured on either side of the choices (d_out x d_in, tokens: us):
+//   8192 x 8192, 1:    K in 2 / 4 / 8 parts 15.8 / 15.3 / 19.2, pair 23.6
+//   1024 x 8192, 1:    K in 1 / 4 / 8 parts 22.0 / 9.5 / 7.4
+//   28672 x 8192, 128: K whole / 2 parts 46.8 / 62.3, pair 53.5
+//   4096 x 4096, 512:  K whole / 2 parts 15.6 / 20.6, pair 18.5
+//   8192 x 8192, 512:  K whole / 2 parts 34.2 / 52.3, pair 29.1
 template <typename Y>
 kronq_status dispatch_mm(const I8MatmulArgs& a, const MmParams& p, cudaStream_t stream) {
-  if (a.n <= 16) return launch_mm<16, Y>(a, p, stream);
-  if (a.n <= 32) return launch_mm<32, Y>(a, p, stream);
-  if (a.n <= 64) return launch_mm<64, Y>(a, p, stream);
-  if (a.n <= 128) return launch_mm<128, Y>(a, p, stream);
-  return launch_mm<256, Y>(a, p, stream);
+  const int sms = device_sms();
+  const int bn = a.n <= 16 ? 16 : a.n <= 32 ? 32 : a.n <= 64 ? 64 : 128;
+  auto up = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
+  const int64_t tiles = up(a.d_out, MM_BM) * up(a.n, bn);
+  int cl = 1;
+  int64_t best = -1;
+  for (int c = 1; c <= 8 && c <= p.kblocks; c *= 2) {
+    const int64_t waves = up(tiles * c, 2 * sms);
+    const int block = tiles * c > sms ? (bn == 128 ? 440 : 300) : (bn == 128 ? 360 : 260);
+    const int64_t cost = waves * (up(p.kblocks, c) * block + 2500) + (c > 1 ? 90 * bn / c : 0);
+    if (best < 0 || cost < best) {
+      best = cost;
+      cl = c;
+    }
+  }
+  const int64_t pair_cost =
+      up(up(a.d_out, 256) * up(a.n, 256), sms / 2) * (static_cast<int64_t>(p.kblocks) * 370 + 2500);
+  // under an SM budget only the pair kernel runs: it alone keeps to a number of SMs
+  if (pair_cost < best || sm_budget() < sms || up(a.d_out, MM_BM) > 65535 || up(a.n, bn) > 65535)
+    return launch_pair<Y>(a, p, stream);
+  switch (bn) {
+    case 16: return launch_split<16, Y>(a, p, cl, stream);
+    case 32: return launch_split<32, Y>(a, p, cl, stream);
+    case 64: return launch_split<64, Y>(a, p, cl, stream);
+    default: return launch_split<128, Y>(a, p, cl, stream);
+  }
 }
 
 }  // namespace

@@ -196,36 +196,47 @@ _BYTES = {torch.uint8: DTYPE_U8, torch.int8: DTYPE_S8}
 
 
 def _float_type(t, name):
-    if t.dtype not in _FLOATS:
+    kind = _FLOATS.get(t.dtype)
+    if kind is None:
         raise ValueError(f"{name} must be bf16 or fp32")
-    return _FLOATS[t.dtype]
-
-
-def _want(name, t, dtype, *shape):
-    """A contiguous tensor of this type and shape, or None, which passes."""
-    if t is None:
-        return
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}")
+    return kind
 
 
 def _rows(name, t, rows, cols):
     """The row stride of a rows x cols matrix with contiguous rows."""
-    if t.dim() != 2 or tuple(t.shape) != (rows, cols) or (cols > 1 and t.stride(1) != 1):
+    if t.shape != (rows, cols) or (cols > 1 and t.stride(1) != 1):
         raise ValueError(f"{name} must be {rows} x {cols} with unit column stride")
-    if rows > 0x7fffffff or cols > 0x7fffffff:
-        raise ValueError(f"{name}: sizes must fit 32 bits")
     return t.stride(0)
 
 
-def _on_one_device(stream, **tensors):
-    """All tensors on the current device: the library launches there."""
-    dev = torch.device("cuda", torch.cuda.current_device())
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the current device is {dev}")
-    if isinstance(stream, torch.cuda.Stream) and stream.device != dev:
-        raise ValueError(f"the stream is on {stream.device}, the current device is {dev}")
+def _sizes(*sizes):
+    if max(sizes) > 0x7fffffff:
+        raise ValueError("sizes must fit 32 bits")
+
+
+# A launch on few tokens takes a few microseconds on the GPU, so these checks cost as little as
+# they can: one pass per tensor, the stream's handle without a Stream object.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _launch_stream(stream, tensors):
+    """The handle of the stream to launch on, after checking that every (name, tensor or None,
+    type or None, length or None) is on the current device, and contiguous of that type and length
+    where one is given (a vector)."""
+    for name, t, dtype, length in tensors:
+        if t is not None and dtype is not None and (
+                t.dtype != dtype or t.dim() != 1 or t.shape[0] != length or
+                (length > 1 and t.stride(0) != 1)):
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of {length} elements")
+    dev = torch.cuda.current_device()
+    for name, t, _, _ in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    if stream is None:
+        return _raw_stream(dev) if _raw_stream is not None else _stream(None)
+    if isinstance(stream, torch.cuda.Stream) and stream.device.index != dev:
+        raise ValueError(f"the stream is on {stream.device}, the current device is cuda:{dev}")
+    return _stream(stream)
 
 
 # ------------------------------------------------------------------------------ status helpers
@@ -465,47 +476,46 @@ def kronq_quantize_tokens(x, q, tok_scale, tok_sum, s_x=None, sign_in=None, flag
     """q (int8), tok_scale, tok_sum of x (n_tok x d_in, bf16 or fp32) after S_X^-1 and V (flags)."""
     lib = load_library()
     n_tok, d_in = x.shape
-    ld_x, ld_q = _rows("x", x, n_tok, d_in), _rows("q", q, n_tok, d_in)
+    _sizes(n_tok, d_in)
+    xd, ld_x, ld_q = _float_type(x, "x"), _rows("x", x, n_tok, d_in), _rows("q", q, n_tok, d_in)
     if q.dtype != torch.int8:
         raise ValueError("q must be int8")
-    _want("tok_scale", tok_scale, torch.float32, n_tok)
-    _want("tok_sum", tok_sum, torch.int32, n_tok)
-    _want("s_x", s_x, torch.float32, d_in)
-    _want("sign_in", sign_in, torch.int8, d_in)
-    xd = _float_type(x, "x")
-    _on_one_device(stream, x=x, q=q, tok_scale=tok_scale, tok_sum=tok_sum, s_x=s_x,
-                   sign_in=sign_in)
-    st = lib.kronq_quantize_tokens(_p(x), xd, ld_x, n_tok, d_in, _p(s_x), _p(sign_in), int(flags),
-                                   _p(q), ld_q, _p(tok_scale), _p(tok_sum), _stream(stream))
-    _check(st, "kronq_quantize_tokens")
+    st = _launch_stream(stream, (("x", x, None, 0), ("q", q, None, 0),
+                                 ("tok_scale", tok_scale, torch.float32, n_tok),
+                                 ("tok_sum", tok_sum, torch.int32, n_tok),
+                                 ("s_x", s_x, torch.float32, d_in),
+                                 ("sign_in", sign_in, torch.int8, d_in)))
+    _check(lib.kronq_quantize_tokens(_p(x), xd, ld_x, n_tok, d_in, _p(s_x), _p(sign_in),
+                                     int(flags), _p(q), ld_q, _p(tok_scale), _p(tok_sum), st),
+           "kronq_quantize_tokens")
 
 
-def _codes_args(codes, scale, zero):
-    d_out, d_in = codes.shape
-    if codes.dtype not in _BYTES:
+def _codes_type(codes):
+    kind = _BYTES.get(codes.dtype)
+    if kind is None:
         raise ValueError("codes must be uint8 or int8")
-    _want("scale", scale, torch.float32, d_out)
-    _want("zero", zero, torch.float32, d_out)
-    return d_out, d_in, _BYTES[codes.dtype], _rows("codes", codes, d_out, d_in)
+    return kind
 
 
 def kronq_matmul_i8(q, tok_scale, tok_sum, codes, scale, zero, y, stream=None):
     """y (n_tok x d_out, fp32 or bf16) = tok_scale scale (q codes^T - zero tok_sum)."""
     lib = load_library()
-    d_out, d_in, cd, ld_codes = _codes_args(codes, scale, zero)
+    d_out, d_in = codes.shape
     n_tok = q.shape[0]
-    ld_q, ld_y = _rows("q", q, n_tok, d_in), _rows("y", y, n_tok, d_out)
+    _sizes(n_tok, d_out, d_in)
+    cd, yd = _codes_type(codes), _float_type(y, "y")
+    ld_codes, ld_q = _rows("codes", codes, d_out, d_in), _rows("q", q, n_tok, d_in)
+    ld_y = _rows("y", y, n_tok, d_out)
     if q.dtype != torch.int8:
         raise ValueError("q must be int8")
-    _want("tok_scale", tok_scale, torch.float32, n_tok)
-    _want("tok_sum", tok_sum, torch.int32, n_tok)
-    yd = _float_type(y, "y")
-    _on_one_device(stream, q=q, tok_scale=tok_scale, tok_sum=tok_sum, codes=codes, scale=scale,
-                   zero=zero, y=y)
-    st = lib.kronq_matmul_i8(_p(q), ld_q, _p(tok_scale), _p(tok_sum), n_tok, _p(codes), cd,
-                             ld_codes, _p(scale), _p(zero), d_out, d_in, _p(y), yd, ld_y,
-                             _stream(stream))
-    _check(st, "kronq_matmul_i8")
+    st = _launch_stream(stream, (("q", q, None, 0), ("codes", codes, None, 0), ("y", y, None, 0),
+                                 ("tok_scale", tok_scale, torch.float32, n_tok),
+                                 ("tok_sum", tok_sum, torch.int32, n_tok),
+                                 ("scale", scale, torch.float32, d_out),
+                                 ("zero", zero, torch.float32, d_out)))
+    _check(lib.kronq_matmul_i8(_p(q), ld_q, _p(tok_scale), _p(tok_sum), n_tok, _p(codes), cd,
+                               ld_codes, _p(scale), _p(zero), d_out, d_in, _p(y), yd, ld_y, st),
+           "kronq_matmul_i8")
 
 
 def kronq_qlinear8_workspace_size(n_tok: int, d_out: int, d_in: int, flags: int) -> int:
@@ -516,22 +526,25 @@ def kronq_qlinear8(x, codes, scale, zero, s_x, s_g, sign_in, sign_out, flags, y,
                    stream=None):
     """y (n_tok x d_out, fp32 or bf16) = S_G^-1 U^T W^' V S_X^-1 x in 8-bit integers."""
     lib = load_library()
-    d_out, d_in, cd, ld_codes = _codes_args(codes, scale, zero)
+    d_out, d_in = codes.shape
     n_tok = x.shape[0]
-    ld_x, ld_y = _rows("x", x, n_tok, d_in), _rows("y", y, n_tok, d_out)
-    for name, t, dtype, d in (("s_x", s_x, torch.float32, d_in), ("s_g", s_g, torch.float32, d_out),
-                              ("sign_in", sign_in, torch.int8, d_in),
-                              ("sign_out", sign_out, torch.int8, d_out)):
-        _want(name, t, dtype, d)
-    xd, yd = _float_type(x, "x"), _float_type(y, "y")
-    _on_one_device(stream, x=x, codes=codes, scale=scale, zero=zero, s_x=s_x, s_g=s_g,
-                   sign_in=sign_in, sign_out=sign_out, y=y, workspace=workspace)
+    _sizes(n_tok, d_out, d_in)
+    cd, xd, yd = _codes_type(codes), _float_type(x, "x"), _float_type(y, "y")
+    ld_codes, ld_x = _rows("codes", codes, d_out, d_in), _rows("x", x, n_tok, d_in)
+    ld_y = _rows("y", y, n_tok, d_out)
+    st = _launch_stream(stream, (("x", x, None, 0), ("codes", codes, None, 0), ("y", y, None, 0),
+                                 ("workspace", workspace, None, 0),
+                                 ("scale", scale, torch.float32, d_out),
+                                 ("zero", zero, torch.float32, d_out),
+                                 ("s_x", s_x, torch.float32, d_in),
+                                 ("s_g", s_g, torch.float32, d_out),
+                                 ("sign_in", sign_in, torch.int8, d_in),
+                                 ("sign_out", sign_out, torch.int8, d_out)))
     ws, wsb = _workspace(lib.kronq_qlinear8_workspace_size(n_tok, d_out, d_in, int(flags)),
                          x.device, workspace)
-    st = lib.kronq_qlinear8(_p(x), xd, ld_x, n_tok, _p(codes), cd, ld_codes, _p(scale), _p(zero),
-                            _p(s_x), _p(s_g), _p(sign_in), _p(sign_out), int(flags), d_out, d_in,
-                            _p(y), yd, ld_y, _p(ws), wsb, _stream(stream))
-    _check(st, "kronq_qlinear8")
+    _check(lib.kronq_qlinear8(_p(x), xd, ld_x, n_tok, _p(codes), cd, ld_codes, _p(scale), _p(zero),
+                              _p(s_x), _p(s_g), _p(sign_in), _p(sign_out), int(flags), d_out, d_in,
+                              _p(y), yd, ld_y, _p(ws), wsb, st), "kronq_qlinear8")
 
 
 # ------------------------------------------------------------------------------ 8. distillation
@@ -541,6 +554,7 @@ def _distill_args(logits, ids, top, dlogits):
     if ids.dim() != 2 or ids.dtype != torch.int32:
         raise ValueError("ids must be a 2-D int32 tensor")
     k = ids.shape[1]
+    _sizes(n_tok, vocab, k)
     head = (_p(logits), _float_type(logits, "logits"), _rows("logits", logits, n_tok, vocab),
             _p(ids), _rows("ids", ids, n_tok, k), _p(top), _float_type(top, "top"),
             _rows("top", top, n_tok, k), n_tok, vocab, k)
@@ -555,14 +569,14 @@ def kronq_distill(logits, ids, top, loss, lse=None, dlogits=None, top_lse=None, 
     entries `ids` (n_tok x k); with dlogits also the gradient, in the same pass over the logits."""
     lib = load_library()
     n_tok, head, grad = _distill_args(logits, ids, top, dlogits)
-    for name, t in (("loss", loss), ("lse", lse), ("top_lse", top_lse),
-                    ("row_weight", row_weight)):
-        _want(name, t, torch.float32, n_tok)
-    _on_one_device(stream, logits=logits, ids=ids, top=top, loss=loss, lse=lse, dlogits=dlogits,
-                   top_lse=top_lse, row_weight=row_weight)
-    st = lib.kronq_distill(*head, _p(top_lse), _p(row_weight), float(temperature), _p(loss),
-                           _p(lse), *grad, _stream(stream))
-    _check(st, "kronq_distill")
+    st = _launch_stream(stream, (("logits", logits, None, 0), ("ids", ids, None, 0),
+                                 ("top", top, None, 0), ("dlogits", dlogits, None, 0),
+                                 ("loss", loss, torch.float32, n_tok),
+                                 ("lse", lse, torch.float32, n_tok),
+                                 ("top_lse", top_lse, torch.float32, n_tok),
+                                 ("row_weight", row_weight, torch.float32, n_tok)))
+    _check(lib.kronq_distill(*head, _p(top_lse), _p(row_weight), float(temperature), _p(loss),
+                             _p(lse), *grad, st), "kronq_distill")
 
 
 def kronq_distill_backward(logits, ids, top, lse, dloss, dlogits, top_lse=None, temperature=1.0,
@@ -570,10 +584,10 @@ def kronq_distill_backward(logits, ids, top, lse, dloss, dlogits, top_lse=None, 
     """dlogits from lse (of kronq_distill) and the upstream gradient dloss per token."""
     lib = load_library()
     n_tok, head, grad = _distill_args(logits, ids, top, dlogits)
-    for name, t in (("lse", lse), ("dloss", dloss), ("top_lse", top_lse)):
-        _want(name, t, torch.float32, n_tok)
-    _on_one_device(stream, logits=logits, ids=ids, top=top, lse=lse, dloss=dloss, dlogits=dlogits,
-                   top_lse=top_lse)
-    st = lib.kronq_distill_backward(*head, _p(top_lse), _p(lse), _p(dloss), float(temperature),
-                                    *grad, _stream(stream))
-    _check(st, "kronq_distill_backward")
+    st = _launch_stream(stream, (("logits", logits, None, 0), ("ids", ids, None, 0),
+                                 ("top", top, None, 0), ("dlogits", dlogits, None, 0),
+                                 ("lse", lse, torch.float32, n_tok),
+                                 ("dloss", dloss, torch.float32, n_tok),
+                                 ("top_lse", top_lse, torch.float32, n_tok)))
+    _check(lib.kronq_distill_backward(*head, _p(top_lse), _p(lse), _p(dloss), float(temperature),
+                                      *grad, st), "kronq_distill_backward")

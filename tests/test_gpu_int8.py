@@ -357,3 +357,28 @@ def test_8bit_layer_of_a_solved_layer(K):
         assert e <= 4.2e-2, e
         errs[bits] = np.einsum("ti,ij,tj->", np64(y) - full, np64(hg), np64(y) - full)
     assert errs[8] < errs[4]
+
+
+@pytest.mark.parametrize("n,d_out,d_in,signed", [(2100, 2561, 400, False), (4096, 2560, 144, True),
+                                                 (700, 9000, 1000, False), (16384, 300, 272, False)])
+def test_matmul_i8_prompts(K, n, d_out, d_in, signed):
+    """Large calls: every output against the exact integer product (fp64 on the device)."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(n + d_out)
+    lo = -128 if signed else 0
+    codes = padded(d_out, d_in, torch.int8 if signed else torch.uint8)
+    codes.copy_(torch.randint(lo, lo + 256, (d_out, d_in), generator=g, device="cuda"))
+    q = padded(n, d_in, torch.int8)
+    q.copy_(torch.randint(-127, 128, (n, d_in), generator=g, device="cuda"))
+    ts = torch.rand(n, generator=g, device="cuda") + 0.1
+    total = q.to(torch.int64).sum(1).to(torch.int32)
+    scale, zero = synth.grid_params(d_out, 0, 8, synth.seed_for("i8pp", n), device="cuda")
+    want = (q.double() @ (codes.double() - zero.double()[:, None]).t()) * ts.double()[:, None] * \
+        scale.double()[None, :]
+    for dtype in (torch.float32, torch.bfloat16):
+        y = torch.full((n, d_out + 3), float("nan"), dtype=dtype, device="cuda")[:, :d_out]
+        K.kronq_matmul_i8(q, ts, total, codes, scale, zero, y)
+        torch.cuda.synchronize()
+        tol = (3.1 * U32 + HALF[dtype]) * want.abs() + 1e-300
+        assert bool(((y.double() - want).abs() <= tol).all())
+    assert K.kronq_device_error() == 0
