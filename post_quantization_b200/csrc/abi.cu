@@ -632,7 +632,7 @@ kronq_status kronq_quantize_tokens(const void* x, int32_t x_dtype, int64_t ld_x,
   const QuantTokensArgs a{x, x_dtype, ld_x, n_tok, d_in,
                           (flags & KRONQ_BIIP_SCALE_IN) ? s_x : nullptr,
                           (flags & KRONQ_BIIP_ROTATE_IN) ? sign_in : nullptr,
-                          q, ld_q, tok_scale, tok_sum};
+                          q, ld_q, tok_scale, tok_sum, 0};
   return run_quant_tokens(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -652,7 +652,7 @@ kronq_status kronq_matmul_i8(const int8_t* q, int64_t ld_q, const float* tok_sca
   KQ_TRY(kronq_device_check());
   const I8MatmulArgs a{q, ld_q, tok_scale, tok_sum, n_tok, codes, ld_codes,
                        codes_dtype == KRONQ_DTYPE_S8, scale, zero, nullptr, d_out, d_in, y,
-                       y_dtype, ld_y};
+                       y_dtype, ld_y, 0, 0};
   return run_i8matmul(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -699,11 +699,11 @@ kronq_status kronq_qlinear8(const void* x, int32_t x_dtype, int64_t ld_x, int32_
     const QuantTokensArgs qa{xt, x_dtype, ld_x, n, d_in,
                              (flags & KRONQ_BIIP_SCALE_IN) ? s_x : nullptr,
                              (flags & KRONQ_BIIP_ROTATE_IN) ? sign_in : nullptr,
-                             q, plan.ld_q, tok_scale, tok_sum};
+                             q, plan.ld_q, tok_scale, tok_sum, 1};
     KQ_TRY(run_quant_tokens(qa, s));
     I8MatmulArgs ma{q, plan.ld_q, tok_scale, tok_sum, n, codes, ld_codes,
                     codes_dtype == KRONQ_DTYPE_S8, scale, zero, rot_out ? nullptr : scale_out,
-                    d_out, d_in, yt, y_dtype, ld_y};
+                    d_out, d_in, yt, y_dtype, ld_y, 1, rot_out};
     if (rot_out) {
       ma.y = yp;
       ma.y_dtype = KRONQ_DTYPE_F32;

@@ -32,6 +32,8 @@ struct MmParams {
   int64_t ld_y;
   int n, d_out, d_in;
   int is_signed;
+  int after_quant;         // the kernel before is the layer's token quantization (see below)
+  int before_transform;    // the kernel behind is the layer's output transform
   int tiles_m, tiles_n, kblocks;
   int* err;
 };
@@ -207,6 +209,12 @@ struct MmCfg {
   static_assert(STAGES * STAGE_BYTES >= BN * MM_BM * 4, "the sums reuse the ring");
 };
 
+__device__ __forceinline__ void mm_wait_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void mm_launch_next() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
 __device__ __forceinline__ uint32_t mm_map(const void* p, uint32_t rank) {
   uint32_t a;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
@@ -269,14 +277,24 @@ __global__ void __launch_bounds__(SP_THREADS, 2)
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer
     if (lane == 0) {
+      // behind the layer's own token quantization, which started after everything before it had
+      // ended, the first stages' weight codes need not wait for the kernel before; the tokens do
+      const int pre = p.after_quant ? min(STAGES, kb1 - kb0) : 0;
+      for (int i = 0; i < pre; ++i) {
+        mbar_arrive_expect_tx(&full[i], C::STAGE_BYTES);
+        tma_load_2d(smem + i * C::STAGE_BYTES, &tma_w, &full[i], (kb0 + i) * MM_BK, tm * MM_BM);
+      }
+      mm_wait_previous();
       int it = 0;
       for (; it < kb1 - kb0; ++it) {
         const int s = it % STAGES;
         const uint32_t ph = (it / STAGES) & 1u;
-        if (!mbar_wait(&empty[s], ph ^ 1u, abort_flag, p.err, DEV_ERR_TMA_WAIT)) break;
         uint8_t* st = smem + s * C::STAGE_BYTES;
-        mbar_arrive_expect_tx(&full[s], C::STAGE_BYTES);
-        tma_load_2d(st, &tma_w, &full[s], (kb0 + it) * MM_BK, tm * MM_BM);
+        if (it >= pre) {
+          if (!mbar_wait(&empty[s], ph ^ 1u, abort_flag, p.err, DEV_ERR_TMA_WAIT)) break;
+          mbar_arrive_expect_tx(&full[s], C::STAGE_BYTES);
+          tma_load_2d(st, &tma_w, &full[s], (kb0 + it) * MM_BK, tm * MM_BM);
+        }
         tma_load_2d(st + C::A_BYTES, &tma_q, &full[s], (kb0 + it) * MM_BK, tn * BN);
       }
       if (it < kb1 - kb0)
@@ -302,11 +320,14 @@ __global__ void __launch_bounds__(SP_THREADS, 2)
       umma_commit(done);
     }
   }
+  if (p.after_quant) c = load_channel(p, ch);
+  mm_wait_previous();
+  if (!p.after_quant) c = load_channel(p, ch);
+  if (p.before_transform) mm_launch_next();
   if (warp >= 2)
     for (int j = threadIdx.x - 64; j < cols; j += SP_THREADS - 64)
       tok[j] = make_float2(p.tok_scale[tn * BN + j],
                            __int_as_float(p.tok_sum ? p.tok_sum[tn * BN + j] : 0));
-  c = load_channel(p, ch);
   __syncwarp();
   const bool ok = mbar_wait(done, 0, abort_flag, p.err, DEV_ERR_EPI_WAIT);
   __syncthreads();     // every role has left its loop; the MMAs and the copies they used are done
@@ -469,6 +490,8 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
   __syncthreads();
   mm_cluster_sync();                                 // the peer's barriers exist
   tc_fence_after();
+  mm_wait_previous();
+  if (p.before_transform) mm_launch_next();
   const uint32_t tmem_base = *tmem_slot;
 
   if (warp == 0) {
@@ -582,22 +605,10 @@ kronq_status launch_pair(const I8MatmulArgs& a, MmParams p, cudaStream_t stream)
   KQ_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                    pr::SMEM_BYTES));
   const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min<int64_t>(tiles, std::max(1, sm_budget() / 2))));
-  cfg.blockDim = dim3(MM_THREADS);
-  cfg.dynamicSmemBytes = pr::SMEM_BYTES;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = 2;
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mw, mq, p);
-  if (e != cudaSuccess)
-    return fail(KRONQ_ERR_CUDA, "i8matmul_pair_kernel: %s", cudaGetErrorString(e));
-  return check_launch("i8matmul_pair_kernel");
+  const unsigned ctas =
+      2 * static_cast<unsigned>(std::min<int64_t>(tiles, std::max(1, sm_budget() / 2)));
+  return launch_chained(kern, dim3(ctas), dim3(MM_THREADS), pr::SMEM_BYTES, stream, 2,
+                        "i8matmul_pair_kernel", mw, mq, p);
 }
 
 template <int BN, typename Y>
@@ -609,22 +620,9 @@ kronq_status launch_split(const I8MatmulArgs& a, const MmParams& p, int cl, cuda
   auto kern = i8matmul_split_kernel<BN, Y>;
   KQ_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                    C::SMEM_BYTES));
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(cl, (a.d_out + MM_BM - 1) / MM_BM, (a.n + BN - 1) / BN);
-  cfg.blockDim = dim3(SP_THREADS);
-  cfg.dynamicSmemBytes = C::SMEM_BYTES;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = static_cast<unsigned>(cl);
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = cl > 1 ? 1 : 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mw, mq, p);
-  if (e != cudaSuccess)
-    return fail(KRONQ_ERR_CUDA, "i8matmul_split_kernel: %s", cudaGetErrorString(e));
-  return check_launch("i8matmul_split_kernel");
+  const dim3 grid(cl, (a.d_out + MM_BM - 1) / MM_BM, (a.n + BN - 1) / BN);
+  return launch_chained(kern, grid, dim3(SP_THREADS), C::SMEM_BYTES, stream, cl,
+                        "i8matmul_split_kernel", mw, mq, p);
 }
 
 // Which kernel, and into how many parts K is cut: by estimated nanoseconds, from measurements on one
@@ -682,6 +680,8 @@ kronq_status run_i8matmul(const I8MatmulArgs& a, cudaStream_t stream) {
   p.d_out = a.d_out;
   p.d_in = a.d_in;
   p.is_signed = a.is_signed;
+  p.after_quant = a.after_quant;
+  p.before_transform = a.before_transform;
   p.kblocks = (a.d_in + MM_BK - 1) / MM_BK;
   p.err = device_error_word();
   if (!p.err) return fail(KRONQ_ERR_CUDA, "device error word unavailable");

@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "../../include/kronq.h"
+#include "common.cuh"
 
 namespace kq {
 
@@ -115,6 +116,7 @@ struct I8MatmulArgs {
   void* y;
   int y_dtype;
   int64_t ld_y;
+  int after_quant, before_transform;   // launched between the layer's other two kernels
 };
 constexpr int kMaxI8Width = 65536;     // 128 * 255 * 65536 < 2^31
 kronq_status run_i8matmul(const I8MatmulArgs& a, cudaStream_t stream);
@@ -131,6 +133,7 @@ struct QuantTokensArgs {
   int64_t ld_q;
   float* tok_scale;
   int32_t* tok_sum;
+  int chained;             // launched in front of the layer's product
 };
 constexpr int kMaxRotatedWidth = 53248;  // a rotated token is held in shared memory (fp32)
 kronq_status run_quant_tokens(const QuantTokensArgs& q, cudaStream_t stream);
@@ -196,6 +199,31 @@ kronq_status tgemm(int m, int n, int k, float alpha, Split3 a, Split3 b, bool b_
 inline Split3 offset(Split3 s, int64_t row, int64_t col) {
   for (int i = 0; i < 3; ++i) s.part[i] += row * s.ld + col;
   return s;
+}
+
+// Launches a kernel that may start while the one before it on the stream still runs (programmatic
+// dependent launch); it waits (griddepcontrol.wait) before it touches what that kernel reads or
+// writes. cluster: CTAs per cluster along x.
+template <typename Kern, typename... Args>
+kronq_status launch_chained(Kern kern, dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                            int cluster, const char* what, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  if (e != cudaSuccess) return fail(KRONQ_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+  return check_launch(what);
 }
 
 inline size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }

@@ -1,9 +1,14 @@
 // The 8-bit layer's element passes: token quantization with the layer's input transforms, and the
 // output transforms.
 //
-//   quant_tokens_kernel   x' = V S_X^-1 x, a = max |x'| per token, s = a / 127,
+//   quant_*_kernel        x' = V S_X^-1 x, a = max |x'| per token, s = a / 127,
 //                         q = rint(x' / s) (of the exact quotient, ties to even), sum = sum q
 //   out_transform_kernel  y = S_G^-1 U^T y' (signs after the Hadamard blocks, which are symmetric)
+//
+// A thread owns units of 8 consecutive elements (16 bytes of bf16, 8 of q), so that a warp's loads
+// and stores are contiguous and the first three Hadamard stages run in its registers; the others go
+// through shared memory in passes of up to four stages (16 elements per thread). Passes of five
+// would save one in some widths but leave threads idle and cost the registers of a third CTA per SM.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -15,59 +20,223 @@
 namespace kq {
 namespace {
 
-constexpr int TQ_THREADS = 512;
+constexpr int TQ_MAX_THREADS = 512;
+constexpr int TQ_CTAS = 3;        // CTAs per SM that the registers leave room for
+constexpr int TQ_THREADS = 256;   // unrotated tokens
+constexpr int TQ_HOLD = 6;        // units a thread keeps there
 
-__device__ __forceinline__ float tq_load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ float tq_load(const float* p) { return *p; }
-__device__ __forceinline__ void tq_store(float* p, float v) { *p = v; }
-__device__ __forceinline__ void tq_store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void tq_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void tq_launch_next() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
 
-// element i of a transformed row sits at i + i / 16: the radix-16 passes below are then free of
-// bank conflicts
+// Eight elements from j0 on, zero past d. VEC: every pointer and row is 16-byte aligned and d is a
+// multiple of 8.
+template <bool VEC>
+__device__ __forceinline__ void tq_load8(const float* p, int j0, int d, float (&v)[8]) {
+  if (VEC) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float4 f = reinterpret_cast<const float4*>(p + j0)[i];
+      v[4 * i] = f.x;
+      v[4 * i + 1] = f.y;
+      v[4 * i + 2] = f.z;
+      v[4 * i + 3] = f.w;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = j0 + e < d ? p[j0 + e] : 0.f;
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void tq_load8(const __nv_bfloat16* p, int j0, int d, float (&v)[8]) {
+  if (VEC) {
+    const uint4 r = *reinterpret_cast<const uint4*>(p + j0);
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[2 * k] = __uint_as_float(w[k] << 16);
+      v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = j0 + e < d ? __bfloat162float(p[j0 + e]) : 0.f;
+  }
+}
+// Eight elements as they lie in memory.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 r;
+  template <bool VEC>
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, int j0, int d) {
+    if (VEC) {
+      r = *reinterpret_cast<const uint4*>(p + j0);
+    } else {
+      const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t lo = j0 + 2 * k < d ? h[j0 + 2 * k] : 0u;
+        const uint32_t hi = j0 + 2 * k + 1 < d ? h[j0 + 2 * k + 1] : 0u;
+        w[k] = lo | (hi << 16);
+      }
+      r = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[2 * k] = __uint_as_float(w[k] << 16);
+      v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+    }
+  }
+};
+template <>
+struct Raw8<float> {
+  float r[8];
+  template <bool VEC>
+  __device__ __forceinline__ void load(const float* p, int j0, int d) {
+    tq_load8<VEC>(p, j0, d, r);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = r[e];
+  }
+};
+template <bool VEC>
+__device__ __forceinline__ void tq_signs8(const int8_t* p, int j0, int d, float (&v)[8]) {
+  uint32_t w[2] = {0u, 0u};
+  if (VEC) {
+    const uint2 r = *reinterpret_cast<const uint2*>(p + j0);
+    w[0] = r.x;
+    w[1] = r.y;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (j0 + e < d) w[e >> 2] |= (static_cast<uint32_t>(p[j0 + e]) & 0xffu) << (8 * (e & 3));
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    v[e] = __uint_as_float(__float_as_uint(v[e]) ^ ((w[e >> 2] << (24 - 8 * (e & 3))) & 0x80000000u));
+}
+template <bool VEC>
+__device__ __forceinline__ void tq_store8(float* p, int j0, int d, const float (&v)[8]) {
+  if (VEC) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      reinterpret_cast<float4*>(p + j0)[i] =
+          make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (j0 + e < d) p[j0 + e] = v[e];
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void tq_store8(__nv_bfloat16* p, int j0, int d, const float (&v)[8]) {
+  if (VEC) {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+      w[k] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *reinterpret_cast<uint4*>(p + j0) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (j0 + e < d) p[j0 + e] = __float2bfloat16_rn(v[e]);
+  }
+}
+
+// Stages of the index bits inside a register array of N elements, for blocks of b.
+template <int N>
+__device__ __forceinline__ void butterflies(float (&v)[N], int b) {
+#pragma unroll
+  for (int h = 1; h < N; h <<= 1) {
+    if (h >= b) break;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (!(j & h)) {
+        const float u = v[j], t = v[j + h];
+        v[j] = u + t;
+        v[j + h] = u - t;
+      }
+  }
+}
+
+// element i of a row in shared memory sits at i + i / 16: the passes are then free of bank conflicts
+// or nearly so
 __device__ __forceinline__ int tq_at(int i) { return i + (i >> 4); }
 
-// Unnormalised Hadamard transform of every aligned block of b (a power of two) elements of the
-// len (a multiple of b) elements in xs. In the pass over index bits [sh, sh + 4) a thread gathers
-// the 16 elements that differ only in those bits and applies four stages in registers.
-__device__ __forceinline__ void hadamard_smem(float* xs, int len, int b) {
-  const int L = 31 - __clz(b);
-  int sh = 0;
-  for (; sh + 4 <= L; sh += 4) {
-    for (int w = threadIdx.x; w < (len >> 4); w += blockDim.x) {
-      const int base = (w & ((1 << sh) - 1)) | ((w >> sh) << (sh + 4));
-      float v[16];
+// Stages of the index bits [SH, SH + R) of len elements (a multiple of 2^(SH + R)). LAST: also the
+// largest magnitude that it leaves (per thread).
+template <int R, int SH, bool LAST>
+__device__ __forceinline__ void hadamard_pass(float* xs, int len, float& amax) {
+  constexpr int N = 1 << R;
+  for (int w = threadIdx.x; w < (len >> R); w += blockDim.x) {
+    float* const p = xs + tq_at((w & ((1 << SH) - 1)) | ((w >> SH) << (SH + R)));
+    // tq_at of 2^SH j past i0 (for SH = 3, i0 mod 16 < 8)
+    auto off = [](int j) { return (j << SH) + ((j << SH) >> 4); };
+    float v[N];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) v[j] = xs[tq_at(base + (j << sh))];
+    for (int j = 0; j < N; ++j) v[j] = p[off(j)];
+    butterflies<N>(v, N);
 #pragma unroll
-      for (int h = 1; h < 16; h <<= 1)
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-          if (!(j & h)) {
-            const float u = v[j], t = v[j + h];
-            v[j] = u + t;
-            v[j + h] = u - t;
-          }
-#pragma unroll
-      for (int j = 0; j < 16; ++j) xs[tq_at(base + (j << sh))] = v[j];
+    for (int j = 0; j < N; ++j) {
+      p[off(j)] = v[j];
+      if (LAST) amax = fmaxf(amax, fabsf(v[j]));
     }
-    __syncthreads();
+    // an infinity or a NaN in a block reaches all of its sums: fmaxf would pass over the NaN, but
+    // one element of the block tells
+    if (LAST && !(fabsf(v[0]) < INFINITY)) amax = INFINITY;
   }
-  for (; sh < L; ++sh) {
-    const int h = 1 << sh;
-    for (int w = threadIdx.x; w < (len >> 1); w += blockDim.x) {
-      const int i = ((w >> sh) << (sh + 1)) | (w & (h - 1));
-      const float u = xs[tq_at(i)], t = xs[tq_at(i + h)];
-      xs[tq_at(i)] = u + t;
-      xs[tq_at(i + h)] = u - t;
-    }
-    __syncthreads();
+  __syncthreads();
+}
+
+// The stages above the first three of every block of 2^L (3 < L <= 15), in passes of equal size.
+// Written out per L, so that every offset is a constant of its instruction.
+__device__ __forceinline__ void hadamard_passes(float* xs, int len, int L, float& amax) {
+  switch (L) {
+    case 4: hadamard_pass<1, 3, true>(xs, len, amax); break;
+    case 5: hadamard_pass<2, 3, true>(xs, len, amax); break;
+    case 6: hadamard_pass<3, 3, true>(xs, len, amax); break;
+    case 7: hadamard_pass<4, 3, true>(xs, len, amax); break;
+    case 8:
+    case 9:
+      hadamard_pass<3, 3, false>(xs, len, amax);
+      if (L == 8) hadamard_pass<2, 6, true>(xs, len, amax);
+      else hadamard_pass<3, 6, true>(xs, len, amax);
+      break;
+    case 12:
+      hadamard_pass<3, 3, false>(xs, len, amax);
+      hadamard_pass<3, 6, false>(xs, len, amax);
+      hadamard_pass<3, 9, true>(xs, len, amax);
+      break;
+    default:
+      hadamard_pass<4, 3, false>(xs, len, amax);
+      if (L == 10) {
+        hadamard_pass<3, 7, true>(xs, len, amax);
+      } else if (L == 11) {
+        hadamard_pass<4, 7, true>(xs, len, amax);
+      } else if (L == 13) {
+        hadamard_pass<3, 7, false>(xs, len, amax);
+        hadamard_pass<3, 10, true>(xs, len, amax);
+      } else {
+        hadamard_pass<4, 7, false>(xs, len, amax);
+        if (L == 14) hadamard_pass<3, 11, true>(xs, len, amax);
+        else hadamard_pass<4, 11, true>(xs, len, amax);
+      }
   }
 }
 
 struct QuantArgs {
   const void* x;
   int64_t ld_x;
-  int d, b;
+  int d, b, log_b;
   const float* s_x;        // NULL: no scaling
   const int8_t* sign_in;   // NULL: no rotation
   float inv_sqrt_b;
@@ -75,6 +244,7 @@ struct QuantArgs {
   int64_t ld_q;
   float* tok_scale;
   int32_t* tok_sum;
+  int chained;             // the kernel behind it is the layer's product: let it start early
 };
 
 // rint(x / s) for |x| <= 127 s (1 + 2^-23) and a normal s, exactly as the real quotient rounds
@@ -89,77 +259,201 @@ __device__ __forceinline__ int quant_code(float x, float s, float inv_s) {
   return static_cast<int>(q);
 }
 
-// One CTA per token.
-template <typename T>
-__global__ void __launch_bounds__(TQ_THREADS) quant_tokens_kernel(QuantArgs a) {
+// Eight codes as two words. x / s is estimated as x inv_s to 2^-16 absolute; adding 1.5 2^23 rounds
+// it to an integer, whose low byte is the float's low byte. Where the estimate lies within 10^-4 of
+// a half (one thread in 600), the exact rounding takes over.
+__device__ __forceinline__ uint2 quant8(const float (&x)[8], float s, float inv_s, int& sum) {
+  constexpr float kMagic = 12582912.f;
+  uint32_t w[2];
+  float off = 0.f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t t[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float f = fmaf(x[4 * i + k], inv_s, kMagic);
+      off = fmaxf(off, fabsf(fmaf(x[4 * i + k], inv_s, -(f - kMagic))));
+      t[k] = __float_as_uint(f);
+    }
+    w[i] = __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
+  }
+  if (off > 0.4999f) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      w[i] = 0u;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        w[i] |= (static_cast<uint32_t>(quant_code(x[4 * i + k], s, inv_s)) & 0xffu) << (8 * k);
+    }
+  }
+  sum = __dp4a(static_cast<int>(w[0]), 0x01010101, sum);
+  sum = __dp4a(static_cast<int>(w[1]), 0x01010101, sum);
+  return make_uint2(w[0], w[1]);
+}
+
+// What both quantization kernels do around a token's transformed values.
+struct TokenScale {
+  float s, inv_s;
+  bool zero;               // no codes: nothing to scale, or not finite
+};
+// From the largest magnitude (as a bit pattern: infinities and NaN come out largest) of each thread.
+__device__ __forceinline__ TokenScale token_scale(uint32_t m, uint32_t* red) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  m = __reduce_max_sync(0xffffffffu, m);
+  if (lane == 0) red[warp] = m;
+  __syncthreads();
+  m = __reduce_max_sync(0xffffffffu, lane < (blockDim.x >> 5) ? red[lane] : 0u);
+  const bool finite = m < 0x7f800000u;
+  TokenScale r;
+  r.s = __uint_as_float(m) / 127.f;
+  r.zero = !finite || r.s < 1.17549435e-38f;
+  if (!finite) r.s = __int_as_float(0x7fc00000);
+  else if (r.zero) r.s = 1.f;
+  r.inv_s = 1.f / r.s;
+  return r;
+}
+template <bool VEC>
+__device__ __forceinline__ void put_codes(int8_t* q, int c, int d, const float (&v)[8],
+                                          const TokenScale& ts, int& sum) {
+  uint2 w = make_uint2(0u, 0u);
+  if (!ts.zero) w = quant8(v, ts.s, ts.inv_s, sum);
+  if (VEC || 8 * c + 8 <= d) {
+    *reinterpret_cast<uint2*>(q + 8 * c) = w;
+  } else {
+    const uint32_t ws[2] = {w.x, w.y};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (8 * c + e < d) q[8 * c + e] = static_cast<int8_t>((ws[e >> 2] >> (8 * (e & 3))) & 0xffu);
+  }
+}
+__device__ __forceinline__ void token_out(const QuantArgs& a, int64_t t, float s, int sum, int* red) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  sum = __reduce_add_sync(0xffffffffu, sum);
+  if (lane == 0) red[warp] = sum;
+  __syncthreads();
+  if (warp == 0) {
+    sum = __reduce_add_sync(0xffffffffu, lane < (blockDim.x >> 5) ? red[lane] : 0);
+    if (lane == 0) {
+      a.tok_scale[t] = s;
+      a.tok_sum[t] = sum;
+    }
+  }
+}
+
+// Tokens whose Hadamard blocks are above 8: one CTA per token, which holds the row in shared memory.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(TQ_MAX_THREADS, TQ_CTAS) quant_rotated_kernel(QuantArgs a) {
   extern __shared__ float xs[];
+  __shared__ uint32_t red_max[TQ_MAX_THREADS / 32];
+  __shared__ int red_sum[TQ_MAX_THREADS / 32];
+  const int64_t t = blockIdx.x;
+  const T* x = static_cast<const T*>(a.x) + t * a.ld_x;
+  const int units = a.d >> 3;
+  tq_wait();                       // x may come from the kernel before
+  if (a.chained) tq_launch_next();
+#pragma unroll 2
+  for (int c = threadIdx.x; c < units; c += blockDim.x) {
+    float v[8];
+    tq_load8<VEC>(x, 8 * c, a.d, v);
+    if (a.s_x) {
+      float s[8];
+      tq_load8<VEC>(a.s_x, 8 * c, a.d, s);
+      // the 2-ulp division: the rotation mixes entries whose roundings differ anyway
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = __fdividef(v[e], s[e]);
+    }
+    tq_signs8<VEC>(a.sign_in, 8 * c, a.d, v);
+    butterflies<8>(v, 8);
+    float* p = xs + tq_at(8 * c);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) p[e] = v[e];
+  }
+  __syncthreads();
+  float amax = 0.f;
+  hadamard_passes(xs, a.d, a.log_b, amax);
+  const TokenScale ts = token_scale(__float_as_uint(amax * a.inv_sqrt_b) & 0x7fffffffu, red_max);
+  int sum = 0;
+  for (int c = threadIdx.x; c < units; c += blockDim.x) {
+    const float* p = xs + tq_at(8 * c);
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = p[e] * a.inv_sqrt_b;
+    put_codes<true>(a.q + t * a.ld_q, c, a.d, v, ts, sum);
+  }
+  token_out(a, t, ts.s, sum, red_sum);
+}
+
+// Tokens without a rotation, or with blocks of at most 8: one CTA per token. A thread keeps its first
+// TQ_HOLD units as they came (all of them up to a width of 12288) and reads others again.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(TQ_THREADS, 4) quant_plain_kernel(QuantArgs a) {
   __shared__ uint32_t red_max[TQ_THREADS / 32];
   __shared__ int red_sum[TQ_THREADS / 32];
   const int64_t t = blockIdx.x;
   const T* x = static_cast<const T*>(a.x) + t * a.ld_x;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const bool rot = a.sign_in != nullptr;
-  auto scaled = [&](int j) {
-    const float v = tq_load(x + j);
-    return a.s_x ? v / a.s_x[j] : v;
-  };
-  if (rot) {
-    for (int j = tid; j < a.d; j += TQ_THREADS) {
-      const float v = scaled(j);
-      xs[tq_at(j)] = a.sign_in[j] < 0 ? -v : v;
+  const int tid = threadIdx.x, nthr = blockDim.x;
+  const int units = (a.d + 7) >> 3;
+  // S_X^-1 x, the signs and the stages
+  auto take = [&](int c, const Raw8<T>& raw, float (&v)[8]) {
+    raw.get(v);
+    if (a.s_x) {
+      float s[8];
+      tq_load8<VEC>(a.s_x, 8 * c, a.d, s);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = VEC || 8 * c + e < a.d ? v[e] / s[e] : 0.f;
     }
-    __syncthreads();
-    hadamard_smem(xs, a.d, a.b);
-  }
-  auto value = [&](int j) { return rot ? xs[tq_at(j)] * a.inv_sqrt_b : scaled(j); };
-  // magnitudes compare as their bit patterns, and infinities and NaN come out largest
+    if (a.sign_in) {
+      tq_signs8<VEC>(a.sign_in, 8 * c, a.d, v);
+      butterflies<8>(v, a.b);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= a.inv_sqrt_b;
+    }
+  };
+  tq_wait();                       // x may come from the kernel before
+  if (a.chained) tq_launch_next();
+  Raw8<T> raw[TQ_HOLD];
+#pragma unroll
+  for (int h = 0; h < TQ_HOLD; ++h)
+    if (tid + h * nthr < units) raw[h].template load<VEC>(x, 8 * (tid + h * nthr), a.d);
   uint32_t m = 0;
-  for (int j = tid; j < a.d; j += TQ_THREADS)
-    m = max(m, __float_as_uint(value(j)) & 0x7fffffffu);
-  m = __reduce_max_sync(0xffffffffu, m);
-  if (lane == 0) red_max[warp] = m;
-  __syncthreads();
-  m = 0;
-  for (int w = 0; w < TQ_THREADS / 32; ++w) m = max(m, red_max[w]);
-  const bool finite = m < 0x7f800000u;
-  float s = __uint_as_float(m) / 127.f;
-  const bool zero = !finite || s < 1.17549435e-38f;
-  if (!finite) s = __int_as_float(0x7fc00000);
-  else if (zero) s = 1.f;
-  const float inv_s = 1.f / s;
+  auto most = [&](int c, const Raw8<T>& r) {
+    float v[8];
+    take(c, r, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[e]) & 0x7fffffffu);
+  };
+#pragma unroll
+  for (int h = 0; h < TQ_HOLD; ++h)
+    if (tid + h * nthr < units) most(tid + h * nthr, raw[h]);
+  for (int c = tid + TQ_HOLD * nthr; c < units; c += nthr) {
+    Raw8<T> r;
+    r.template load<VEC>(x, 8 * c, a.d);
+    most(c, r);
+  }
+  const TokenScale ts = token_scale(m, red_max);
   int sum = 0;
   int8_t* q = a.q + t * a.ld_q;
-  for (int j0 = tid * 16; j0 < a.d; j0 += TQ_THREADS * 16) {
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      int c = 0;
-      if (j0 + e < a.d && !zero) c = quant_code(value(j0 + e), s, inv_s);
-      sum += c;
-      w[e >> 2] |= (static_cast<uint32_t>(c) & 0xffu) << (8 * (e & 3));
+  for (int h = 0; h < TQ_HOLD; ++h)
+    if (tid + h * nthr < units) {
+      float v[8];
+      take(tid + h * nthr, raw[h], v);
+      put_codes<VEC>(q, tid + h * nthr, a.d, v, ts, sum);
     }
-    if (j0 + 16 <= a.d) {
-      *reinterpret_cast<uint4*>(q + j0) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-      for (int e = 0; j0 + e < a.d; ++e)
-        q[j0 + e] = static_cast<int8_t>((w[e >> 2] >> (8 * (e & 3))) & 0xffu);
-    }
+  for (int c = tid + TQ_HOLD * nthr; c < units; c += nthr) {
+    Raw8<T> r;
+    r.template load<VEC>(x, 8 * c, a.d);
+    float v[8];
+    take(c, r, v);
+    put_codes<VEC>(q, c, a.d, v, ts, sum);
   }
-  sum = __reduce_add_sync(0xffffffffu, sum);
-  if (lane == 0) red_sum[warp] = sum;
-  __syncthreads();
-  if (tid == 0) {
-    int tot = 0;
-    for (int w = 0; w < TQ_THREADS / 32; ++w) tot += red_sum[w];
-    a.tok_scale[t] = s;
-    a.tok_sum[t] = tot;
-  }
+  token_out(a, t, ts.s, sum, red_sum);
 }
 
 struct OutArgs {
   const float* yp;
   int64_t ld_yp;
-  int d, b, span;
+  int d, b, log_b, span;
   const float* s_g;        // NULL: no scaling
   const int8_t* sign_out;
   float inv_sqrt_b;
@@ -168,26 +462,72 @@ struct OutArgs {
 };
 
 // One CTA per (token, span of whole Hadamard blocks).
-template <typename Y>
-__global__ void __launch_bounds__(256) out_transform_kernel(OutArgs a) {
+template <typename Y, bool VEC>
+__global__ void __launch_bounds__(TQ_MAX_THREADS, TQ_CTAS) out_transform_kernel(OutArgs a) {
   extern __shared__ float xs[];
   const int64_t t = blockIdx.y;
   const int j0 = blockIdx.x * a.span;
   const int len = min(a.span, a.d - j0);
+  const int units = (len + 7) >> 3;
   const float* yp = a.yp + t * a.ld_yp + j0;
-  for (int j = threadIdx.x; j < len; j += blockDim.x) xs[tq_at(j)] = yp[j];
-  __syncthreads();
-  hadamard_smem(xs, len, a.b);
   Y* y = static_cast<Y*>(a.y) + t * a.ld_y + j0;
-  for (int j = threadIdx.x; j < len; j += blockDim.x) {
-    float v = xs[tq_at(j)] * (a.sign_out[j0 + j] < 0 ? -a.inv_sqrt_b : a.inv_sqrt_b);
-    if (a.s_g) v = v / a.s_g[j0 + j];
-    tq_store(y + j, v);
+  auto finish = [&](int c, float (&v)[8]) {
+    tq_signs8<VEC>(a.sign_out + j0, 8 * c, len, v);
+    if (a.s_g) {
+      float s[8];
+      tq_load8<VEC>(a.s_g + j0, 8 * c, len, s);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = __fdividef(v[e] * a.inv_sqrt_b, s[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= a.inv_sqrt_b;
+    }
+    tq_store8<VEC>(y, 8 * c, len, v);
+  };
+  tq_wait();
+  if (a.b <= 8) {
+    for (int c = threadIdx.x; c < units; c += blockDim.x) {
+      float v[8];
+      tq_load8<VEC>(yp, 8 * c, len, v);
+      butterflies<8>(v, a.b);
+      finish(c, v);
+    }
+    return;
+  }
+#pragma unroll 2
+  for (int c = threadIdx.x; c < units; c += blockDim.x) {
+    float v[8];
+    tq_load8<VEC>(yp, 8 * c, len, v);
+    butterflies<8>(v, 8);
+    float* p = xs + tq_at(8 * c);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) p[e] = v[e];
+  }
+  __syncthreads();
+  float unused = 0.f;
+  hadamard_passes(xs, len, a.log_b, unused);
+  for (int c = threadIdx.x; c < units; c += blockDim.x) {
+    const float* p = xs + tq_at(8 * c);
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = p[e];
+    finish(c, v);
   }
 }
 
-size_t padded_floats(int len) { return static_cast<size_t>(len) + len / 16 + 1; }
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// threads for `units` units of 8: two a thread, evenly
+int unit_threads(int units) {
+  const int per = std::max(2, (units + TQ_MAX_THREADS - 1) / TQ_MAX_THREADS);
+  return std::max(32, ((units + per - 1) / per + 31) / 32 * 32);
+}
 int pow2_part(int d) { return d & (-d); }
+int log2_of(int b) {
+  int l = 0;
+  while ((1 << l) < b) ++l;
+  return l;
+}
+size_t row_smem(int len) { return static_cast<size_t>(17) * ((len + 15) / 16) * sizeof(float); }   // tq_at
 
 }  // namespace
 
@@ -197,6 +537,7 @@ kronq_status run_quant_tokens(const QuantTokensArgs& q, cudaStream_t stream) {
   a.ld_x = q.ld_x;
   a.d = q.d;
   a.b = pow2_part(q.d);
+  a.log_b = log2_of(a.b);
   a.s_x = q.s_x;
   a.sign_in = q.sign_in;
   a.inv_sqrt_b = static_cast<float>(1.0 / std::sqrt(static_cast<double>(a.b)));
@@ -204,16 +545,28 @@ kronq_status run_quant_tokens(const QuantTokensArgs& q, cudaStream_t stream) {
   a.ld_q = q.ld_q;
   a.tok_scale = q.tok_scale;
   a.tok_sum = q.tok_sum;
-  const size_t smem = q.sign_in ? padded_floats(q.d) * sizeof(float) : 0;
+  a.chained = q.chained;
+  const bool smem_row = q.sign_in && a.b > 8;
+  const size_t smem = smem_row ? row_smem(q.d) : 0;
+  const bool vec = q.d % 8 == 0 && aligned16(q.x) && (q.n == 1 || q.ld_x % 8 == 0) &&
+                   aligned16(q.s_x) && aligned16(q.sign_in);
+  const int units = (q.d + 7) / 8;
+  // unrotated: two units a thread as far as TQ_THREADS go
+  const int threads = smem_row ? unit_threads(units)
+                               : std::min(TQ_THREADS, std::max(32, ((units + 1) / 2 + 31) / 32 * 32));
   auto launch = [&](auto kern) -> kronq_status {
     if (smem > 48 * 1024)
       KQ_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem)));
-    kern<<<q.n, TQ_THREADS, smem, stream>>>(a);
-    return check_launch("quant_tokens_kernel");
+    return launch_chained(kern, dim3(q.n), dim3(threads), smem, stream, 1, "quantize_tokens kernel", a);
   };
-  return q.x_dtype == KRONQ_DTYPE_BF16 ? launch(quant_tokens_kernel<__nv_bfloat16>)
-                                       : launch(quant_tokens_kernel<float>);
+  auto typed = [&](auto x) -> kronq_status {
+    using T = decltype(x);
+    if (smem_row)
+      return vec ? launch(quant_rotated_kernel<T, true>) : launch(quant_rotated_kernel<T, false>);
+    return vec ? launch(quant_plain_kernel<T, true>) : launch(quant_plain_kernel<T, false>);
+  };
+  return q.x_dtype == KRONQ_DTYPE_BF16 ? typed(__nv_bfloat16()) : typed(0.f);
 }
 
 kronq_status run_out_transform(const float* yp, int64_t ld_yp, int n, int d, const float* s_g,
@@ -224,24 +577,29 @@ kronq_status run_out_transform(const float* yp, int64_t ld_yp, int n, int d, con
   a.ld_yp = ld_yp;
   a.d = d;
   a.b = pow2_part(d);
-  a.span = a.b;
+  a.log_b = log2_of(a.b);
+  a.span = std::max(a.b, 16);
   while (a.span < 1024 && a.span < d) a.span *= 2;
   a.s_g = s_g;
   a.sign_out = sign_out;
   a.inv_sqrt_b = static_cast<float>(1.0 / std::sqrt(static_cast<double>(a.b)));
   a.y = y;
   a.ld_y = ld_y;
-  const size_t smem = padded_floats(a.span) * sizeof(float);
+  const size_t smem = a.b > 8 ? row_smem(a.span) : 0;
+  const bool vec = d % 8 == 0 && aligned16(yp) && ld_yp % 4 == 0 && aligned16(y) &&
+                   (n == 1 || ld_y % 8 == 0) && aligned16(s_g) && aligned16(sign_out);
   const dim3 grid((d + a.span - 1) / a.span, n);
   auto launch = [&](auto kern) -> kronq_status {
     if (smem > 48 * 1024)
       KQ_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem)));
-    kern<<<grid, 256, smem, stream>>>(a);
-    return check_launch("out_transform_kernel");
+    return launch_chained(kern, grid, dim3(unit_threads(a.span / 8)), smem, stream, 1,
+                          "out_transform_kernel", a);
   };
-  return y_dtype == KRONQ_DTYPE_BF16 ? launch(out_transform_kernel<__nv_bfloat16>)
-                                     : launch(out_transform_kernel<float>);
+  if (y_dtype == KRONQ_DTYPE_BF16)
+    return vec ? launch(out_transform_kernel<__nv_bfloat16, true>)
+               : launch(out_transform_kernel<__nv_bfloat16, false>);
+  return vec ? launch(out_transform_kernel<float, true>) : launch(out_transform_kernel<float, false>);
 }
 
 }  // namespace kq
