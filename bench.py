@@ -59,9 +59,10 @@ def parse():
     ap.add_argument("--overlap", type=int, default=0, metavar="SMS",
                     help="overlapped schedule with SMS SMs kept free of statistics for the "
                          "chains (0: no reservation)")
-    ap.add_argument("--calibration", default="synthetic", choices=["synthetic", "backward"],
+    ap.add_argument("--calibration", default="synthetic", choices=["synthetic", "backward", "distill"],
                     help="synthetic: seeded X and G generators; backward: X and G of every linear "
-                         "from the forward and backward of a random-weight block")
+                         "from the forward and backward of a random-weight block; distill: the "
+                         "same with a distillation loss in place of a random output gradient")
     ap.add_argument("--hg-diag", action="store_true",
                     help="diagonal-only H_G: sum diag(G^T G) in one streaming pass instead of "
                          "the G^T G product (BiIP's scales and the trace need only the diagonal)")
@@ -291,10 +292,12 @@ class Block:
                                        dtype=wl.w_dtype, device=device) for s in wl.sublayers}
         # X~ (the quantized model's input) in self.x; with the asymmetric term on, also X (the
         # full-precision model's input) in self.xfp, and D = (X - X~)^T X~ per stream
-        if calibration == "backward":
-            # X and G from the forward and backward of a random-weight block with these weights
-            xs, gs = synth.block_calibration(wl, n_tokens, synth.seed_for(tag, "block"),
-                                             device=device, weights=self.w)
+        if calibration in ("backward", "distill"):
+            # X and G from the forward and backward of a random-weight block with these weights,
+            # from a random gradient of its output or from a distillation loss
+            xs, gs = synth.block_calibration(
+                wl, n_tokens, synth.seed_for(tag, "block"), device=device, weights=self.w,
+                distill=synth.Distillation() if calibration == "distill" else None)
         else:
             xs = {name: synth.correlated_x(n_tokens, d, synth.seed_for(tag, name, "X"),
                                            device=device) for name, d in wl.streams().items()}
@@ -722,9 +725,13 @@ def run_gpu(args):
                        "schedule": ("overlapped" + (f", {blk.reserve} SMs reserved"
                                                     if blk.reserve else "")
                                     if blk.overlap else "phases"),
-                       "calibration": ("X and G from the forward and backward of a random-weight "
-                                       "block" if args.calibration == "backward" else
-                                       "seeded synthetic X and G"),
+                       "calibration": {
+                           "synthetic": "seeded synthetic X and G",
+                           "backward": "X and G from the forward and backward of a random-weight "
+                                       "block",
+                           "distill": "X and G from the forward and backward of a random-weight "
+                                      "block with weights rounded to 4 bits, from its distillation "
+                                      "loss against the block itself"}[args.calibration],
                        "hg": "diagonal only" if args.hg_diag else "full G^T G",
                        "l2": f"inputs ({blk.input_bytes() / 1e9:.0f} GB) larger than L2"},
             "accumulate_tflops": acc_tflops,

@@ -11,6 +11,10 @@
         the comparison variant with output-side feedback against the column solve
     python -m post_quantization_b200.profcase qlinear --block --bits 2 --group 128 --tokens 1
         the quantized layers at inference, per layer (graph replays) and as one block sweep
+    python -m post_quantization_b200.profcase qlinear8 --tokens 2048
+        the LLaMA-3-70B block's linears in 8-bit integers, per layer and for the block
+    python -m post_quantization_b200.profcase distill --tokens 4096 --vocab 128256 --top-k 128
+        the distillation loss alone, with its gradient, and the gradient from a given lse
 Each case runs its call `--reps` times (default 3) after one warm-up call.
 """
 from __future__ import annotations
@@ -429,10 +433,87 @@ def case_qlinear(args):
     del graphs
 
 
+def replay_us(fn, reps):
+    """Microseconds per call of fn, captured in a CUDA graph and replayed `reps` times."""
+    stream = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(stream):
+        fn()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=stream):
+            fn()
+    for _ in range(3):
+        graph.replay()
+    a, b = ev(), ev()
+    torch.cuda.synchronize()
+    a.record()
+    for _ in range(reps):
+        graph.replay()
+    b.record()
+    torch.cuda.synchronize()
+    return a.elapsed_time(b) * 1e3 / reps
+
+
+def case_qlinear8(args):
+    """The linears of one LLaMA-3-70B-shaped block in 8-bit integers, all transforms on; the block's
+    codes (0.86 GB) exceed L2."""
+    dev = torch.device("cuda")
+    n = args.tokens or 1
+    out = []
+    for nm, do, di in LLAMA3_70B_LINEARS:
+        tag = ("qlinear8-case", nm)
+        c = synth.codes(do, di, 8, synth.seed_for(tag, "c"), device=dev)
+        scale, zero = synth.grid_params(do, 0, 8, synth.seed_for(tag, "g"), device=dev)
+        layer = P.Linear8(c, scale, zero, synth.positive_scales(di, synth.seed_for(tag, "sx"),
+                                                                device=dev),
+                          synth.positive_scales(do, synth.seed_for(tag, "sg"), device=dev),
+                          synth.rademacher(di, synth.seed_for(tag, "si"), device=dev),
+                          synth.rademacher(do, synth.seed_for(tag, "so"), device=dev))
+        x = synth.activations(n, di, synth.seed_for(tag, "x"), dtype=torch.bfloat16, device=dev)
+        out.append((nm, layer, x, torch.empty(n, do, dtype=torch.bfloat16, device=dev)))
+    ws = P.Workspace(dev)
+    reps = max(args.reps, 10)
+    rows = {}
+    for nm, layer, x, y in out:
+        do, di = layer.codes.shape
+        us = replay_us(lambda: layer(x, y=y, ws=ws), reps)
+        rows[nm] = {"us": us, "tb_s": (do * di + 2 * n * (do + di)) / us / 1e6,
+                    "tops": 2.0 * n * do * di / us / 1e6}
+
+    def block():
+        for _, layer, x, y in out:
+            layer(x, y=y, ws=ws)
+    us = replay_us(block, reps)
+    print(json.dumps({"case": "qlinear8", "tokens": n, "layers": rows, "block_us": us}))
+
+
+def case_distill(args):
+    dev = torch.device("cuda")
+    n, v, k = args.tokens or 4096, args.vocab, args.top_k
+    g = torch.Generator(device=dev)
+    g.manual_seed(synth.seed_for("distill-case"))
+    z = torch.empty(n, v, dtype=torch.bfloat16, device=dev)
+    for r in range(0, n, 1024):
+        z[r:r + 1024] = 2.0 * torch.randn(min(1024, n - r), v, generator=g, device=dev)
+    top, ids = z[:, :].topk(k, dim=1)
+    ids = ids.to(torch.int32)
+    loss, lse = torch.empty(n, device=dev), torch.empty(n, device=dev)
+    dz, one = torch.empty_like(z), torch.ones(n, device=dev)
+    reps = max(args.reps, 10)
+    res = {"loss": replay_us(lambda: K.kronq_distill(z, ids, top, loss, lse), reps),
+           "loss_and_gradient": replay_us(
+               lambda: K.kronq_distill(z, ids, top, loss, lse, dlogits=dz), reps),
+           "gradient": replay_us(
+               lambda: K.kronq_distill_backward(z, ids, top, lse, one, dz), reps)}
+    nbytes = {"loss": 2 * n * v, "loss_and_gradient": 4 * n * v, "gradient": 4 * n * v}
+    print(json.dumps({"case": "distill", "tokens": n, "vocab": v, "top_k": k, "dtype": "bf16",
+                      "us": res, "tb_s": {m: nbytes[m] / us / 1e6 for m, us in res.items()}}))
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("case", choices=["stages", "acc", "biip", "cholinv", "quantize", "qlinear",
-                                     "peaks", "twosided"])
+                                     "peaks", "twosided", "qlinear8", "distill"])
     ap.add_argument("--drift", action="store_true", help="acc: the drift sum D alone; "
                                                           "quantize: with D (P pre-shift)")
     ap.add_argument("--tokens", type=int, default=None)
@@ -444,12 +525,15 @@ def main():
     ap.add_argument("--bits", type=int, default=2, help="qlinear: code width")
     ap.add_argument("--block", action="store_true", help="qlinear: the LLaMA-3-70B block")
     ap.add_argument("--no-graphs", action="store_true", help="qlinear: eager calls")
+    ap.add_argument("--vocab", type=int, default=128256, help="distill")
+    ap.add_argument("--top-k", type=int, default=128, help="distill")
     args = ap.parse_args()
     K.load_library()
     K.kronq_device_check()
     {"stages": stages, "acc": case_acc, "biip": case_biip, "cholinv": case_cholinv,
      "quantize": case_quantize, "qlinear": case_qlinear, "peaks": case_peaks,
-     "twosided": case_twosided}[args.case](args)
+     "twosided": case_twosided, "qlinear8": case_qlinear8,
+     "distill": case_distill}[args.case](args)
 
 
 if __name__ == "__main__":

@@ -256,9 +256,28 @@ def _rms_norm(x: torch.Tensor, eps: float = 1e-5) -> torch.Tensor:
     return x * torch.rsqrt(x.pow(2).mean(dim=-1, keepdim=True) + eps)
 
 
+@dataclass(frozen=True)
+class Distillation:
+    """The loss of a calibration backward: the full-precision block's top logits, over a random
+    output head, teach the block with rounded weights."""
+    vocab: int = 32000
+    top_k: int = 64
+    temperature: float = 1.0
+    bits: int = 4                # the student's weights: rounded to a b-bit grid per row
+
+
+def rounded(w: torch.Tensor, bits: int) -> torch.Tensor:
+    """w rounded to the nearest point of a b-bit min-max grid per row (no solve)."""
+    f = w.float()
+    lo, hi = f.amin(1, keepdim=True), f.amax(1, keepdim=True)
+    step = ((hi - lo) / ((1 << bits) - 1)).clamp(min=1e-30)
+    return (((f - lo) / step).round() * step + lo).to(w.dtype)
+
+
 def block_calibration(wl: Workload, n: int, seed: int, device="cpu", seq_len: int = 2048,
                       head_dim: int = 128, seqs_per_chunk: int = 4, dtype=torch.bfloat16,
-                      weights: dict | None = None):
+                      weights: dict | None = None, distill: Distillation | None = None,
+                      losses: torch.Tensor | None = None):
     """X (per input stream) and G (per sublayer) of one forward + backward of a random-weight block.
 
     Block: u = x + o_proj(attn(q_proj(n1), k_proj(n1), v_proj(n1))) with n1 = rmsnorm(x), causal
@@ -269,7 +288,15 @@ def block_calibration(wl: Workload, n: int, seed: int, device="cpu", seq_len: in
     N(0, 0.02^2) in wl's shapes, or `weights` ({sublayer: W}) when given, so that the statistics
     belong to the layers being quantized. Returns ({stream: X}, {sublayer: G}) with the streams
     of wl: the inputs of q/k/v, o, gate/up and down.
+
+    With `distill` the gradient of the block output is that of a loss instead (CUDA only): the
+    block's own output, normalised, times a random output head gives the teacher's logits, whose
+    top ones are kept; the same block with rounded weights is the student, and kronq_distill gives
+    its loss per token (written to `losses`, fp32 of n, when given) and the gradient of its logits.
+    X and G are then the student's.
     """
+    if distill is not None and torch.device(device).type != "cuda":
+        raise ValueError("distillation runs on the GPU library: device must be CUDA")
     subs = {s.name: s for s in wl.sublayers}
     h = subs["q_proj"].d_in
     heads = subs["q_proj"].d_out // head_dim
@@ -279,7 +306,13 @@ def block_calibration(wl: Workload, n: int, seed: int, device="cpu", seq_len: in
         name: weight(s.d_out, s.d_in, seed_for(seed, name, "W"), dtype=dtype, device=device)
         for name, s in subs.items()}
     x_all = correlated_x(n, h, seed_for(seed, "x"), dtype=dtype, device=device)
-    gy_all = gradients(n, h, seed_for(seed, "gy"), dtype=dtype, device=device)
+    if distill is None:
+        gy_all = gradients(n, h, seed_for(seed, "gy"), dtype=dtype, device=device)
+    else:
+        from . import kronq as K
+        teacher = {name: v.to(f32) for name, v in w.items()}
+        w = {name: rounded(v, distill.bits) for name, v in w.items()}
+        head = weight(distill.vocab, h, seed_for(seed, "head"), dtype=dtype, device=device).to(f32)
     stream_of = {s.name: s.x_stream for s in wl.sublayers}
     xs = {st: torch.empty(n, subs[name].d_in, dtype=dtype, device=device)
           for name, st in stream_of.items()}
@@ -297,7 +330,7 @@ def block_calibration(wl: Workload, n: int, seed: int, device="cpu", seq_len: in
             outs[name] = (inp, out)
             return out
 
-        with torch.enable_grad():
+        def forward(lin):
             n1 = _rms_norm(x)
             q = lin("q_proj", n1)
             k = lin("k_proj", n1)
@@ -314,8 +347,26 @@ def block_calibration(wl: Workload, n: int, seed: int, device="cpu", seq_len: in
             n2 = _rms_norm(u)
             a = lin("gate_proj", n2)
             b = lin("up_proj", n2)
-            y = u + lin("down_proj", torch.nn.functional.silu(a) * b)
-            y.backward(gy_all[c0:c1].to(f32))
+            return u + lin("down_proj", torch.nn.functional.silu(a) * b)
+
+        if distill is None:
+            with torch.enable_grad():
+                y = forward(lin)
+                y.backward(gy_all[c0:c1].to(f32))
+        else:
+            with torch.no_grad():
+                yt = forward(lambda name, inp: inp @ teacher[name].t())
+                top, ids = (_rms_norm(yt) @ head.t()).topk(distill.top_k, dim=1)
+            with torch.enable_grad():
+                ny = _rms_norm(forward(lin))
+                logits = (ny.detach() @ head.t()).to(dtype)
+                loss = torch.empty(c1 - c0, dtype=f32, device=device)
+                K.kronq_distill(logits, ids.to(torch.int32), top, loss, dlogits=logits,
+                                temperature=distill.temperature)
+                ny.backward(logits.to(f32) @ head)
+            if losses is not None:
+                losses[c0:c1] = loss
+            del yt, ny, logits
         for name, (inp, out) in outs.items():
             xs[stream_of[name]][c0:c1] = inp.detach().to(dtype)
             gs[name][c0:c1] = out.grad.to(dtype)
