@@ -1134,10 +1134,11 @@ kronq_status launch_distill(DsArgs a, int n, bool lse, bool grad, cudaStream_t s
   constexpr int NV = 8;
   const int64_t vecs = static_cast<int64_t>(a.v) / Vec<T>::VE + 1;    // at most, and at least one
   if (!lse) {
-    // the gradient alone has no statistics to exchange: any number of slices, here of four
-    // vectors per thread
-    a.per = 4 * DS_THREADS;
-    a.cl = static_cast<int>((vecs + a.per - 1) / a.per);
+    // the gradient alone has no statistics to exchange: any number of slices, of at least four
+    // vectors per thread, but no more than give every SM twelve CTAs (each works through the list)
+    const int64_t most = std::max<int64_t>(1, (12LL * device_sms() + n - 1) / n);
+    a.cl = static_cast<int>(std::max<int64_t>(1, std::min((vecs + 4 * DS_THREADS - 1) / (4 * DS_THREADS), most)));
+    a.per = static_cast<int>((vecs + a.cl - 1) / a.cl);
     return launch_rows(distill_stream_kernel<T, D, false, true, KPT>, a, n, false, true,
                        "distill_stream_kernel", stream);
   }
