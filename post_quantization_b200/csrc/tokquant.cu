@@ -85,6 +85,12 @@ struct Raw8<__nv_bfloat16> {
       r = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
+  // the largest magnitude's bit pattern as fp32 (infinities and NaN come out largest)
+  __device__ __forceinline__ uint32_t most() const {
+    const uint32_t k = 0x7fff7fffu;
+    const uint32_t m = __vmaxu2(__vmaxu2(r.x & k, r.y & k), __vmaxu2(r.z & k, r.w & k));
+    return max(m << 16, m & 0xffff0000u);
+  }
   __device__ __forceinline__ void get(float (&v)[8]) const {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
@@ -100,6 +106,12 @@ struct Raw8<float> {
   template <bool VEC>
   __device__ __forceinline__ void load(const float* p, int j0, int d) {
     tq_load8<VEC>(p, j0, d, r);
+  }
+  __device__ __forceinline__ uint32_t most() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(r[e]) & 0x7fffffffu);
+    return m;
   }
   __device__ __forceinline__ void get(float (&v)[8]) const {
 #pragma unroll
@@ -168,19 +180,27 @@ __device__ __forceinline__ void butterflies(float (&v)[N], int b) {
   }
 }
 
-// element i of a row in shared memory sits at i + i / 16: the passes are then free of bank conflicts
-// or nearly so
-__device__ __forceinline__ int tq_at(int i) { return i + (i >> 4); }
+// Element i of a row in shared memory sits at i + i / 32: the 8 consecutive elements of 32 threads,
+// and 32 consecutive elements, lie in different banks.
+__device__ __forceinline__ int tq_at(int i) { return i + (i >> 5); }
 
 // Stages of the index bits [SH, SH + R) of len elements (a multiple of 2^(SH + R)). LAST: also the
 // largest magnitude that it leaves (per thread).
 template <int R, int SH, bool LAST>
 __device__ __forceinline__ void hadamard_pass(float* xs, int len, float& amax) {
   constexpr int N = 1 << R;
+  // In the first pass (SH = 3) eight threads share the low bits; four groups of them would meet in
+  // the same banks 2^(3 + R) apart, and do not 256 apart: the bits of w above 3 that a warp counts
+  // through become index bits 8 and 9.
+  constexpr int B8 = SH == 3 ? 5 - R : 0;            // bits between 3 + R and 8
+  const bool spread = SH == 3 && (len & 1023) == 0;
   for (int w = threadIdx.x; w < (len >> R); w += blockDim.x) {
-    float* const p = xs + tq_at((w & ((1 << SH) - 1)) | ((w >> SH) << (SH + R)));
-    // tq_at of 2^SH j past i0 (for SH = 3, i0 mod 16 < 8)
-    auto off = [](int j) { return (j << SH) + ((j << SH) >> 4); };
+    int hi = w >> SH;
+    if (spread)
+      hi = (hi & ~((4 << B8) - 1)) | ((hi & 3) << B8) | ((hi >> 2) & ((1 << B8) - 1));
+    float* const p = xs + tq_at((w & ((1 << SH) - 1)) | (hi << (SH + R)));
+    // tq_at of 2^SH j past it (for SH = 3 its low five bits are below 8)
+    auto off = [](int j) { return (j << SH) + ((j << SH) >> 5); };
     float v[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) v[j] = p[off(j)];
@@ -259,21 +279,48 @@ __device__ __forceinline__ int quant_code(float x, float s, float inv_s) {
   return static_cast<int>(q);
 }
 
+// ---- pairs of fp32 in one 64-bit register pair (packed arithmetic)
+__device__ __forceinline__ uint64_t tq_pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 tq_unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t tq_fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t tq_add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // Eight codes as two words. x / s is estimated as x inv_s to 2^-16 absolute; adding 1.5 2^23 rounds
 // it to an integer, whose low byte is the float's low byte. Where the estimate lies within 10^-4 of
 // a half (one thread in 600), the exact rounding takes over.
 __device__ __forceinline__ uint2 quant8(const float (&x)[8], float s, float inv_s, int& sum) {
-  constexpr float kMagic = 12582912.f;
+  const uint64_t magic = tq_pack2(12582912.f, 12582912.f), unmagic = tq_pack2(-12582912.f, -12582912.f);
+  const uint64_t inv2 = tq_pack2(inv_s, inv_s), neg2 = tq_pack2(-inv_s, -inv_s);
   uint32_t w[2];
   float off = 0.f;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     uint32_t t[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float f = fmaf(x[4 * i + k], inv_s, kMagic);
-      off = fmaxf(off, fabsf(fmaf(x[4 * i + k], inv_s, -(f - kMagic))));
-      t[k] = __float_as_uint(f);
+    for (int k = 0; k < 2; ++k) {
+      const uint64_t v = tq_pack2(x[4 * i + 2 * k], x[4 * i + 2 * k + 1]);
+      const uint64_t f = tq_fma2(v, inv2, magic);
+      const float2 d = tq_unpack2(tq_fma2(v, neg2, tq_add2(f, unmagic)));   // -(x inv_s - q)
+      off = fmaxf(off, fmaxf(fabsf(d.x), fabsf(d.y)));
+      const float2 b = tq_unpack2(f);
+      t[2 * k] = __float_as_uint(b.x);
+      t[2 * k + 1] = __float_as_uint(b.y);
     }
     w[i] = __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
   }
@@ -416,7 +463,12 @@ __global__ void __launch_bounds__(TQ_THREADS, 4) quant_plain_kernel(QuantArgs a)
   for (int h = 0; h < TQ_HOLD; ++h)
     if (tid + h * nthr < units) raw[h].template load<VEC>(x, 8 * (tid + h * nthr), a.d);
   uint32_t m = 0;
+  const bool plain = !a.s_x && !a.sign_in;
   auto most = [&](int c, const Raw8<T>& r) {
+    if (plain) {
+      m = max(m, r.most());
+      return;
+    }
     float v[8];
     take(c, r, v);
 #pragma unroll
@@ -527,7 +579,7 @@ int log2_of(int b) {
   while ((1 << l) < b) ++l;
   return l;
 }
-size_t row_smem(int len) { return static_cast<size_t>(17) * ((len + 15) / 16) * sizeof(float); }   // tq_at
+size_t row_smem(int len) { return static_cast<size_t>(33) * ((len + 31) / 32) * sizeof(float); }   // tq_at
 
 }  // namespace
 
