@@ -602,8 +602,8 @@ kronq_status launch_pair(const I8MatmulArgs& a, MmParams p, cudaStream_t stream)
   KQ_TRY(byte_map(&mw, a.codes, a.ld_codes, a.d_in, a.d_out, 128));
   KQ_TRY(byte_map(&mq, a.q, a.ld_q, a.d_in, a.n, 128));
   auto kern = i8matmul_pair_kernel<Y>;
-  KQ_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   pr::SMEM_BYTES));
+  static std::atomic<uint64_t> allowed{0};
+  KQ_TRY(allow_smem(reinterpret_cast<const void*>(kern), pr::SMEM_BYTES, allowed));
   const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
   const unsigned ctas =
       2 * static_cast<unsigned>(std::min<int64_t>(tiles, std::max(1, sm_budget() / 2)));
@@ -618,8 +618,8 @@ kronq_status launch_split(const I8MatmulArgs& a, const MmParams& p, int cl, cuda
   KQ_TRY(byte_map(&mw, a.codes, a.ld_codes, a.d_in, a.d_out, MM_BM));
   KQ_TRY(byte_map(&mq, a.q, a.ld_q, a.d_in, a.n, BN));
   auto kern = i8matmul_split_kernel<BN, Y>;
-  KQ_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   C::SMEM_BYTES));
+  static std::atomic<uint64_t> allowed{0};
+  KQ_TRY(allow_smem(reinterpret_cast<const void*>(kern), C::SMEM_BYTES, allowed));
   const dim3 grid(cl, (a.d_out + MM_BM - 1) / MM_BM, (a.n + BN - 1) / BN);
   return launch_chained(kern, grid, dim3(SP_THREADS), C::SMEM_BYTES, stream, cl,
                         "i8matmul_split_kernel", mw, mq, p);

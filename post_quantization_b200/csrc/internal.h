@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/kronq.h"
 #include "common.cuh"
 
@@ -199,6 +201,19 @@ kronq_status tgemm(int m, int n, int k, float alpha, Split3 a, Split3 b, bool b_
 inline Split3 offset(Split3 s, int64_t row, int64_t col) {
   for (int i = 0; i < 3; ++i) s.part[i] += row * s.ld + col;
   return s;
+}
+
+// Lets a kernel take `bytes` of dynamic shared memory: once per device and kernel (`done`:
+// a static of the caller's, one bit per device), so bytes is the most that it is launched with.
+inline kronq_status allow_smem(const void* kern, size_t bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  KQ_CUDA_TRY(cudaGetDevice(&dev));
+  const uint64_t bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_relaxed) & bit) return KRONQ_OK;
+  KQ_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   static_cast<int>(bytes)));
+  if (dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+  return KRONQ_OK;
 }
 
 // Launches a kernel that may start while the one before it on the stream still runs (programmatic

@@ -204,9 +204,12 @@ def _float_type(t, name):
 
 def _rows(name, t, rows, cols):
     """The row stride of a rows x cols matrix with contiguous rows."""
-    if t.shape != (rows, cols) or (cols > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be {rows} x {cols} with unit column stride")
-    return t.stride(0)
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} must be {rows} x {cols}")
+    ld, one = t.stride()
+    if one != 1 and cols > 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return ld
 
 
 def _sizes(*sizes):
@@ -219,23 +222,26 @@ def _sizes(*sizes):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _launch_stream(stream, tensors):
-    """The handle of the stream to launch on, after checking that every (name, tensor or None,
-    type or None, length or None) is on the current device, and contiguous of that type and length
-    where one is given (a vector)."""
-    for name, t, dtype, length in tensors:
-        if t is not None and dtype is not None and (
-                t.dtype != dtype or t.dim() != 1 or t.shape[0] != length or
-                (length > 1 and t.stride(0) != 1)):
-            raise ValueError(f"{name} must be a contiguous {dtype} tensor of {length} elements")
-    dev = torch.cuda.current_device()
-    for name, t, _, _ in tensors:
+def _launch_stream(stream, first, tensors, vectors):
+    """The handle of the stream to launch on, after checking that all tensors (or None) are on the
+    current device, and the vectors (name, tensor or None, type, length) contiguous of that type."""
+    dev = first.get_device()
+    for t in tensors:
         if t is not None and t.get_device() != dev:
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+    for name, t, dtype, length in vectors:
+        if t is None:
+            continue
+        if t.dtype != dtype or t.shape != (length,) or (length > 1 and t.stride(0) != 1):
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of {length} elements")
+        if t.get_device() != dev:
+            raise ValueError(f"tensors on {first.device} and {t.device} ({name})")
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError(f"tensors on {first.device}, which is not the current CUDA device")
     if stream is None:
         return _raw_stream(dev) if _raw_stream is not None else _stream(None)
     if isinstance(stream, torch.cuda.Stream) and stream.device.index != dev:
-        raise ValueError(f"the stream is on {stream.device}, the current device is cuda:{dev}")
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {first.device}")
     return _stream(stream)
 
 
@@ -474,17 +480,16 @@ def kronq_qlinear(x, packed, packed_grid, s_x, s_g, sign_in, sign_out, flags, d_
 
 def kronq_quantize_tokens(x, q, tok_scale, tok_sum, s_x=None, sign_in=None, flags=0, stream=None):
     """q (int8), tok_scale, tok_sum of x (n_tok x d_in, bf16 or fp32) after S_X^-1 and V (flags)."""
-    lib = load_library()
+    lib = _lib or load_library()
     n_tok, d_in = x.shape
     _sizes(n_tok, d_in)
     xd, ld_x, ld_q = _float_type(x, "x"), _rows("x", x, n_tok, d_in), _rows("q", q, n_tok, d_in)
     if q.dtype != torch.int8:
         raise ValueError("q must be int8")
-    st = _launch_stream(stream, (("x", x, None, 0), ("q", q, None, 0),
-                                 ("tok_scale", tok_scale, torch.float32, n_tok),
-                                 ("tok_sum", tok_sum, torch.int32, n_tok),
-                                 ("s_x", s_x, torch.float32, d_in),
-                                 ("sign_in", sign_in, torch.int8, d_in)))
+    st = _launch_stream(stream, x, (q,), (("tok_scale", tok_scale, torch.float32, n_tok),
+                                          ("tok_sum", tok_sum, torch.int32, n_tok),
+                                          ("s_x", s_x, torch.float32, d_in),
+                                          ("sign_in", sign_in, torch.int8, d_in)))
     _check(lib.kronq_quantize_tokens(_p(x), xd, ld_x, n_tok, d_in, _p(s_x), _p(sign_in),
                                      int(flags), _p(q), ld_q, _p(tok_scale), _p(tok_sum), st),
            "kronq_quantize_tokens")
@@ -499,7 +504,7 @@ def _codes_type(codes):
 
 def kronq_matmul_i8(q, tok_scale, tok_sum, codes, scale, zero, y, stream=None):
     """y (n_tok x d_out, fp32 or bf16) = tok_scale scale (q codes^T - zero tok_sum)."""
-    lib = load_library()
+    lib = _lib or load_library()
     d_out, d_in = codes.shape
     n_tok = q.shape[0]
     _sizes(n_tok, d_out, d_in)
@@ -508,11 +513,10 @@ def kronq_matmul_i8(q, tok_scale, tok_sum, codes, scale, zero, y, stream=None):
     ld_y = _rows("y", y, n_tok, d_out)
     if q.dtype != torch.int8:
         raise ValueError("q must be int8")
-    st = _launch_stream(stream, (("q", q, None, 0), ("codes", codes, None, 0), ("y", y, None, 0),
-                                 ("tok_scale", tok_scale, torch.float32, n_tok),
-                                 ("tok_sum", tok_sum, torch.int32, n_tok),
-                                 ("scale", scale, torch.float32, d_out),
-                                 ("zero", zero, torch.float32, d_out)))
+    st = _launch_stream(stream, q, (codes, y), (("tok_scale", tok_scale, torch.float32, n_tok),
+                                                ("tok_sum", tok_sum, torch.int32, n_tok),
+                                                ("scale", scale, torch.float32, d_out),
+                                                ("zero", zero, torch.float32, d_out)))
     _check(lib.kronq_matmul_i8(_p(q), ld_q, _p(tok_scale), _p(tok_sum), n_tok, _p(codes), cd,
                                ld_codes, _p(scale), _p(zero), d_out, d_in, _p(y), yd, ld_y, st),
            "kronq_matmul_i8")
@@ -525,21 +529,19 @@ def kronq_qlinear8_workspace_size(n_tok: int, d_out: int, d_in: int, flags: int)
 def kronq_qlinear8(x, codes, scale, zero, s_x, s_g, sign_in, sign_out, flags, y, workspace=None,
                    stream=None):
     """y (n_tok x d_out, fp32 or bf16) = S_G^-1 U^T W^' V S_X^-1 x in 8-bit integers."""
-    lib = load_library()
+    lib = _lib or load_library()
     d_out, d_in = codes.shape
     n_tok = x.shape[0]
     _sizes(n_tok, d_out, d_in)
     cd, xd, yd = _codes_type(codes), _float_type(x, "x"), _float_type(y, "y")
     ld_codes, ld_x = _rows("codes", codes, d_out, d_in), _rows("x", x, n_tok, d_in)
     ld_y = _rows("y", y, n_tok, d_out)
-    st = _launch_stream(stream, (("x", x, None, 0), ("codes", codes, None, 0), ("y", y, None, 0),
-                                 ("workspace", workspace, None, 0),
-                                 ("scale", scale, torch.float32, d_out),
-                                 ("zero", zero, torch.float32, d_out),
-                                 ("s_x", s_x, torch.float32, d_in),
-                                 ("s_g", s_g, torch.float32, d_out),
-                                 ("sign_in", sign_in, torch.int8, d_in),
-                                 ("sign_out", sign_out, torch.int8, d_out)))
+    st = _launch_stream(stream, x, (codes, y, workspace),
+                        (("scale", scale, torch.float32, d_out),
+                         ("zero", zero, torch.float32, d_out),
+                         ("s_x", s_x, torch.float32, d_in), ("s_g", s_g, torch.float32, d_out),
+                         ("sign_in", sign_in, torch.int8, d_in),
+                         ("sign_out", sign_out, torch.int8, d_out)))
     ws, wsb = _workspace(lib.kronq_qlinear8_workspace_size(n_tok, d_out, d_in, int(flags)),
                          x.device, workspace)
     _check(lib.kronq_qlinear8(_p(x), xd, ld_x, n_tok, _p(codes), cd, ld_codes, _p(scale), _p(zero),
@@ -567,14 +569,12 @@ def kronq_distill(logits, ids, top, loss, lse=None, dlogits=None, top_lse=None, 
                   temperature=1.0, stream=None):
     """loss (and lse) of student logits (n_tok x vocab) against the teacher's top logits `top` at
     entries `ids` (n_tok x k); with dlogits also the gradient, in the same pass over the logits."""
-    lib = load_library()
+    lib = _lib or load_library()
     n_tok, head, grad = _distill_args(logits, ids, top, dlogits)
-    st = _launch_stream(stream, (("logits", logits, None, 0), ("ids", ids, None, 0),
-                                 ("top", top, None, 0), ("dlogits", dlogits, None, 0),
-                                 ("loss", loss, torch.float32, n_tok),
-                                 ("lse", lse, torch.float32, n_tok),
-                                 ("top_lse", top_lse, torch.float32, n_tok),
-                                 ("row_weight", row_weight, torch.float32, n_tok)))
+    st = _launch_stream(stream, logits, (ids, top, dlogits),
+                        (("loss", loss, torch.float32, n_tok), ("lse", lse, torch.float32, n_tok),
+                         ("top_lse", top_lse, torch.float32, n_tok),
+                         ("row_weight", row_weight, torch.float32, n_tok)))
     _check(lib.kronq_distill(*head, _p(top_lse), _p(row_weight), float(temperature), _p(loss),
                              _p(lse), *grad, st), "kronq_distill")
 
@@ -582,12 +582,10 @@ def kronq_distill(logits, ids, top, loss, lse=None, dlogits=None, top_lse=None, 
 def kronq_distill_backward(logits, ids, top, lse, dloss, dlogits, top_lse=None, temperature=1.0,
                            stream=None):
     """dlogits from lse (of kronq_distill) and the upstream gradient dloss per token."""
-    lib = load_library()
+    lib = _lib or load_library()
     n_tok, head, grad = _distill_args(logits, ids, top, dlogits)
-    st = _launch_stream(stream, (("logits", logits, None, 0), ("ids", ids, None, 0),
-                                 ("top", top, None, 0), ("dlogits", dlogits, None, 0),
-                                 ("lse", lse, torch.float32, n_tok),
-                                 ("dloss", dloss, torch.float32, n_tok),
-                                 ("top_lse", top_lse, torch.float32, n_tok)))
+    st = _launch_stream(stream, logits, (ids, top, dlogits),
+                        (("lse", lse, torch.float32, n_tok), ("dloss", dloss, torch.float32, n_tok),
+                         ("top_lse", top_lse, torch.float32, n_tok)))
     _check(lib.kronq_distill_backward(*head, _p(top_lse), _p(lse), _p(dloss), float(temperature),
                                       *grad, st), "kronq_distill_backward")
