@@ -692,8 +692,8 @@ kronq_status kronq_qlinear8(const void* x, int32_t x_dtype, int64_t ld_x, int32_
   int32_t* tok_sum = reinterpret_cast<int32_t*>(w + plan.q_bytes + plan.tok_bytes);
   float* yp = reinterpret_cast<float*>(w + plan.q_bytes + 2 * plan.tok_bytes);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  for (int32_t t0 = 0; t0 < n_tok; t0 += plan.chunk) {
-    const int32_t n = std::min(plan.chunk, n_tok - t0);
+  for (int64_t t0 = 0; t0 < n_tok; t0 += plan.chunk) {
+    const int32_t n = static_cast<int32_t>(std::min<int64_t>(plan.chunk, n_tok - t0));
     const uint8_t* xt = static_cast<const uint8_t*>(x) + t0 * ld_x * dtype_bytes(x_dtype);
     uint8_t* yt = static_cast<uint8_t*>(y) + t0 * ld_y * dtype_bytes(y_dtype);
     const QuantTokensArgs qa{xt, x_dtype, ld_x, n, d_in,

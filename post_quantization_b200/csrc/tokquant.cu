@@ -164,19 +164,70 @@ __device__ __forceinline__ void tq_store8(__nv_bfloat16* p, int j0, int d, const
   }
 }
 
-// Stages of the index bits inside a register array of N elements, for blocks of b.
+// ---- pairs of fp32 in one 64-bit register pair (packed arithmetic)
+__device__ __forceinline__ uint64_t tq_pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 tq_unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t tq_fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t tq_add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t tq_sub2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// a / b to 2 ulp (b normal, below 2^126)
+__device__ __forceinline__ float tq_quotient(float a, float b) {
+  float r;
+  asm("div.approx.ftz.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Stages of the index bits inside a register array of N elements, for blocks of b: the first between
+// neighbours, the others on pairs.
 template <int N>
 __device__ __forceinline__ void butterflies(float (&v)[N], int b) {
+  if (b == 1) return;
+  if constexpr (N == 2) {
+    const float u = v[0], t = v[1];
+    v[0] = u + t;
+    v[1] = u - t;
+  } else {
+    uint64_t p[N / 2];
 #pragma unroll
-  for (int h = 1; h < N; h <<= 1) {
-    if (h >= b) break;
+    for (int j = 0; j < N / 2; ++j) p[j] = tq_pack2(v[2 * j] + v[2 * j + 1], v[2 * j] - v[2 * j + 1]);
 #pragma unroll
-    for (int j = 0; j < N; ++j)
-      if (!(j & h)) {
-        const float u = v[j], t = v[j + h];
-        v[j] = u + t;
-        v[j + h] = u - t;
-      }
+    for (int h = 1; h < N / 2; h <<= 1) {
+      if (2 * h >= b) break;
+#pragma unroll
+      for (int j = 0; j < N / 2; ++j)
+        if (!(j & h)) {
+          const uint64_t u = p[j], t = p[j + h];
+          p[j] = tq_add2(u, t);
+          p[j + h] = tq_sub2(u, t);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) {
+      const float2 f = tq_unpack2(p[j]);
+      v[2 * j] = f.x;
+      v[2 * j + 1] = f.y;
+    }
   }
 }
 
@@ -277,28 +328,6 @@ __device__ __forceinline__ int quant_code(float x, float s, float inv_s) {
   if (r > s || (r == s && (static_cast<int>(q0) & 1))) q += 1.f;
   if (r < -s || (r == -s && (static_cast<int>(q0) & 1))) q -= 1.f;
   return static_cast<int>(q);
-}
-
-// ---- pairs of fp32 in one 64-bit register pair (packed arithmetic)
-__device__ __forceinline__ uint64_t tq_pack2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 tq_unpack2(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t tq_fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t tq_add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
 }
 
 // Eight codes as two words. x / s is estimated as x inv_s to 2^-16 absolute; adding 1.5 2^23 rounds
@@ -407,7 +436,7 @@ __global__ void __launch_bounds__(TQ_MAX_THREADS, TQ_CTAS) quant_rotated_kernel(
       tq_load8<VEC>(a.s_x, 8 * c, a.d, s);
       // the 2-ulp division: the rotation mixes entries whose roundings differ anyway
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = __fdividef(v[e], s[e]);
+      for (int e = 0; e < 8; ++e) v[e] = tq_quotient(v[e], s[e]);
     }
     tq_signs8<VEC>(a.sign_in, 8 * c, a.d, v);
     butterflies<8>(v, 8);
@@ -529,7 +558,7 @@ __global__ void __launch_bounds__(TQ_MAX_THREADS, TQ_CTAS) out_transform_kernel(
       float s[8];
       tq_load8<VEC>(a.s_g + j0, 8 * c, len, s);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = __fdividef(v[e] * a.inv_sqrt_b, s[e]);
+      for (int e = 0; e < 8; ++e) v[e] = tq_quotient(v[e] * a.inv_sqrt_b, s[e]);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] *= a.inv_sqrt_b;
