@@ -420,8 +420,9 @@ KRONQ_API kronq_status kronq_qlinear(const void* x, int32_t x_dtype, int64_t ld_
  *   tok_scale (device, fp32), tok_sum (device, int32): n_tok each
  *   Arithmetic: x' in fp32; s_t = max|x'| / 127 rounded once; q is the exact quotient x' / s_t
  *   rounded to the nearest integer, ties to even, so |q| <= 127. A token whose s_t would be below
- *   2^-126 (all zero, say) has q = 0, s_t = 1. A token with an infinity or a NaN in x' has q = 0
- *   and s_t = NaN, which makes its whole output row NaN. */
+ *   2^-126 (all zero, say) has q = 0, s_t = 1. A token with an infinity or a NaN in x' (with
+ *   ROTATE_IN also in a sum of a Hadamard block, sqrt(block) x') has q = 0 and s_t = NaN, which
+ *   makes its whole output row NaN. s_x (and s_g below) are positive normal numbers below 2^126. */
 KRONQ_API kronq_status kronq_quantize_tokens(const void* x, int32_t x_dtype, int64_t ld_x,
                                              int32_t n_tok, int32_t d_in, const float* s_x,
                                              const int8_t* sign_in, uint32_t flags, int8_t* q,

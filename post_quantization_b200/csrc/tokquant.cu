@@ -5,10 +5,15 @@
 //                         q = rint(x' / s) (of the exact quotient, ties to even), sum = sum q
 //   out_transform_kernel  y = S_G^-1 U^T y' (signs after the Hadamard blocks, which are symmetric)
 //
-// A thread owns units of 8 consecutive elements (16 bytes of bf16, 8 of q), so that a warp's loads
-// and stores are contiguous and the first three Hadamard stages run in its registers; the others go
-// through shared memory in passes of up to four stages (16 elements per thread). Passes of five
-// would save one in some widths but leave threads idle and cost the registers of a third CTA per SM.
+// Hadamard stages commute, so each of them runs where its elements share a thread. A row takes three
+// phases, with the row in shared memory between them:
+//   groups   of 4 neighbours, and for long blocks 2, 4 or 8 of them that differ in the top bits of
+//            their place in the block (2 bits, and up to 3 from the top)
+//   columns  2 .. 32 elements that are 32 apart (index bits 5 .. 9)
+//   strips   of 32 neighbours (bits 2 .. 4, or 0 .. 4)
+// Groups touch device memory in whole lines, with the channel scales and signs they need, columns do
+// for fp32. The token pass ends with the strips, which stay in registers until the token's scale is
+// known; the output pass takes columns, strips, groups.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -20,12 +25,16 @@
 namespace kq {
 namespace {
 
-constexpr int TQ_MAX_THREADS = 512;
-constexpr int TQ_CTAS = 3;        // CTAs per SM that the registers leave room for
+constexpr int TQ_MAX_THREADS = 384;
+constexpr int TQ_CTAS = 2;        // of that size per SM (85 registers a thread)
+constexpr int UNIT_THREADS = 512; // out_units_kernel
 constexpr int TQ_THREADS = 256;   // unrotated tokens
 constexpr int TQ_HOLD = 6;        // units a thread keeps there
 
 __device__ __forceinline__ void tq_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void tq_prefetch(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
 __device__ __forceinline__ void tq_launch_next() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
@@ -231,77 +240,86 @@ __device__ __forceinline__ void butterflies(float (&v)[N], int b) {
   }
 }
 
-// Element i of a row in shared memory sits at i + i / 32: the 8 consecutive elements of 32 threads,
-// and 32 consecutive elements, lie in different banks.
-__device__ __forceinline__ int tq_at(int i) { return i + (i >> 5); }
+// Stages of the pair-index bits h = LO, 2 LO .. below HI of a pair array (element bits one higher).
+template <int N>
+__device__ __forceinline__ void pair_stages(uint64_t (&p)[N], int lo, int hi) {
+#pragma unroll
+  for (int h = 1; h < N; h <<= 1) {
+    if (h < lo || h >= hi) continue;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (!(j & h)) {
+        const uint64_t u = p[j], t = p[j + h];
+        p[j] = tq_add2(u, t);
+        p[j + h] = tq_sub2(u, t);
+      }
+  }
+}
 
-// Stages of the index bits [SH, SH + R) of len elements (a multiple of 2^(SH + R)). LAST: also the
-// largest magnitude that it leaves (per thread).
-template <int R, int SH, bool LAST>
-__device__ __forceinline__ void hadamard_pass(float* xs, int len, float& amax) {
+// The row in shared memory: strips of 32 elements, whose 8 groups of 4 are permuted by the strip's
+// number, so that neighbouring groups, the same group of neighbouring strips and the columns of a
+// strip all lie in different banks. Word offset of element e:
+__device__ __forceinline__ int tq_at(int e) {
+  return (e & ~31) | ((e ^ (((e >> 5) & 7) << 2)) & 31);
+}
+__device__ __forceinline__ ulonglong2* tq_group(float* xs, int g) {
+  return reinterpret_cast<ulonglong2*>(xs + tq_at(4 * g));
+}
+__device__ __forceinline__ void strip_get(float* xs, int c, uint64_t (&p)[16]) {
+#pragma unroll
+  for (int g = 0; g < 8; ++g) {
+    const ulonglong2 w = *tq_group(xs, 8 * c + g);
+    p[2 * g] = w.x;
+    p[2 * g + 1] = w.y;
+  }
+}
+__device__ __forceinline__ void strip_put(float* xs, int c, const uint64_t (&p)[16]) {
+#pragma unroll
+  for (int g = 0; g < 8; ++g) *tq_group(xs, 8 * c + g) = make_ulonglong2(p[2 * g], p[2 * g + 1]);
+}
+
+// Stages of the index bits [SH, SH + R) of len elements (a multiple of 2^(SH + R), SH >= 5), in
+// shared memory or, with GLOBAL, taken from device memory.
+template <int R, int SH, bool GLOBAL>
+__device__ __forceinline__ void column_pass(float* xs, const float* from, int len) {
   constexpr int N = 1 << R;
-  // In the first pass (SH = 3) eight threads share the low bits; four groups of them would meet in
-  // the same banks 2^(3 + R) apart, and do not 256 apart: the bits of w above 3 that a warp counts
-  // through become index bits 8 and 9.
-  constexpr int B8 = SH == 3 ? 5 - R : 0;            // bits between 3 + R and 8
-  const bool spread = SH == 3 && (len & 1023) == 0;
+#pragma unroll(N < 16 ? 16 / N : 1)
   for (int w = threadIdx.x; w < (len >> R); w += blockDim.x) {
-    int hi = w >> SH;
-    if (spread)
-      hi = (hi & ~((4 << B8) - 1)) | ((hi & 3) << B8) | ((hi >> 2) & ((1 << B8) - 1));
-    float* const p = xs + tq_at((w & ((1 << SH) - 1)) | (hi << (SH + R)));
-    // tq_at of 2^SH j past it (for SH = 3 its low five bits are below 8)
-    auto off = [](int j) { return (j << SH) + ((j << SH) >> 5); };
+    const int e = (w & ((1 << SH) - 1)) | ((w >> SH) << (SH + R));
     float v[N];
 #pragma unroll
-    for (int j = 0; j < N; ++j) v[j] = p[off(j)];
+    for (int j = 0; j < N; ++j) v[j] = GLOBAL ? from[e + (j << SH)] : xs[tq_at(e | (j << SH))];
     butterflies<N>(v, N);
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      p[off(j)] = v[j];
-      if (LAST) amax = fmaxf(amax, fabsf(v[j]));
-    }
-    // an infinity or a NaN in a block reaches all of its sums: fmaxf would pass over the NaN, but
-    // one element of the block tells
-    if (LAST && !(fabsf(v[0]) < INFINITY)) amax = INFINITY;
+    for (int j = 0; j < N; ++j) xs[tq_at(e | (j << SH))] = v[j];
   }
   __syncthreads();
 }
-
-// The stages above the first three of every block of 2^L (3 < L <= 15), in passes of equal size.
-// Written out per L, so that every offset is a constant of its instruction.
-__device__ __forceinline__ void hadamard_passes(float* xs, int len, int L, float& amax) {
+// Bits 5 .. 9 of blocks of 2^L, in shared memory.
+__device__ __forceinline__ void columns(float* xs, int len, int L) {
   switch (L) {
-    case 4: hadamard_pass<1, 3, true>(xs, len, amax); break;
-    case 5: hadamard_pass<2, 3, true>(xs, len, amax); break;
-    case 6: hadamard_pass<3, 3, true>(xs, len, amax); break;
-    case 7: hadamard_pass<4, 3, true>(xs, len, amax); break;
-    case 8:
-    case 9:
-      hadamard_pass<3, 3, false>(xs, len, amax);
-      if (L == 8) hadamard_pass<2, 6, true>(xs, len, amax);
-      else hadamard_pass<3, 6, true>(xs, len, amax);
-      break;
-    case 12:
-      hadamard_pass<3, 3, false>(xs, len, amax);
-      hadamard_pass<3, 6, false>(xs, len, amax);
-      hadamard_pass<3, 9, true>(xs, len, amax);
-      break;
-    default:
-      hadamard_pass<4, 3, false>(xs, len, amax);
-      if (L == 10) {
-        hadamard_pass<3, 7, true>(xs, len, amax);
-      } else if (L == 11) {
-        hadamard_pass<4, 7, true>(xs, len, amax);
-      } else if (L == 13) {
-        hadamard_pass<3, 7, false>(xs, len, amax);
-        hadamard_pass<3, 10, true>(xs, len, amax);
-      } else {
-        hadamard_pass<4, 7, false>(xs, len, amax);
-        if (L == 14) hadamard_pass<3, 11, true>(xs, len, amax);
-        else hadamard_pass<4, 11, true>(xs, len, amax);
-      }
+    case 4:
+    case 5: break;
+    case 6: column_pass<1, 5, false>(xs, xs, len); break;
+    case 7: column_pass<2, 5, false>(xs, xs, len); break;
+    case 8: column_pass<3, 5, false>(xs, xs, len); break;
+    case 9: column_pass<4, 5, false>(xs, xs, len); break;
+    default: column_pass<5, 5, false>(xs, xs, len);
   }
+}
+// What columns, strips and three top bits leave of blocks above 8192.
+__device__ __forceinline__ void middle_bits(float* xs, int len, int L) {
+  if (L == 14) column_pass<1, 10, false>(xs, xs, len);
+  if (L == 15) column_pass<2, 10, false>(xs, xs, len);
+}
+// The top bits that the groups take.
+int top_bits(int log_b) { return std::min(3, std::max(0, log_b - 10)); }
+
+// Largest magnitude; a NaN stays.
+__device__ __forceinline__ float max_abs(float m, float v) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
+  return r;
 }
 
 struct QuantArgs {
@@ -330,12 +348,14 @@ __device__ __forceinline__ int quant_code(float x, float s, float inv_s) {
   return static_cast<int>(q);
 }
 
-// Eight codes as two words. x / s is estimated as x inv_s to 2^-16 absolute; adding 1.5 2^23 rounds
-// it to an integer, whose low byte is the float's low byte. Where the estimate lies within 10^-4 of
-// a half (one thread in 600), the exact rounding takes over.
-__device__ __forceinline__ uint2 quant8(const float (&x)[8], float s, float inv_s, int& sum) {
+// Eight codes as two words, of x = fl(v pre). x / s is estimated as v fl(pre inv_s), to 3 2^-17
+// absolute; adding 1.5 2^23 rounds it to an integer, whose low byte is the float's low byte. Where the
+// estimate lies within 10^-4 of a half (one thread in 600), the exact rounding takes over.
+__device__ __forceinline__ uint2 quant8(const float (&x)[8], float pre, float s, float inv_s,
+                                        int& sum) {
+  const float est = pre * inv_s;
   const uint64_t magic = tq_pack2(12582912.f, 12582912.f), unmagic = tq_pack2(-12582912.f, -12582912.f);
-  const uint64_t inv2 = tq_pack2(inv_s, inv_s), neg2 = tq_pack2(-inv_s, -inv_s);
+  const uint64_t inv2 = tq_pack2(est, est), neg2 = tq_pack2(-est, -est);
   uint32_t w[2];
   float off = 0.f;
 #pragma unroll
@@ -345,7 +365,7 @@ __device__ __forceinline__ uint2 quant8(const float (&x)[8], float s, float inv_
     for (int k = 0; k < 2; ++k) {
       const uint64_t v = tq_pack2(x[4 * i + 2 * k], x[4 * i + 2 * k + 1]);
       const uint64_t f = tq_fma2(v, inv2, magic);
-      const float2 d = tq_unpack2(tq_fma2(v, neg2, tq_add2(f, unmagic)));   // -(x inv_s - q)
+      const float2 d = tq_unpack2(tq_fma2(v, neg2, tq_add2(f, unmagic)));   // -(x / s - q)
       off = fmaxf(off, fmaxf(fabsf(d.x), fabsf(d.y)));
       const float2 b = tq_unpack2(f);
       t[2 * k] = __float_as_uint(b.x);
@@ -359,7 +379,7 @@ __device__ __forceinline__ uint2 quant8(const float (&x)[8], float s, float inv_
       w[i] = 0u;
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        w[i] |= (static_cast<uint32_t>(quant_code(x[4 * i + k], s, inv_s)) & 0xffu) << (8 * k);
+        w[i] |= (static_cast<uint32_t>(quant_code(x[4 * i + k] * pre, s, inv_s)) & 0xffu) << (8 * k);
     }
   }
   sum = __dp4a(static_cast<int>(w[0]), 0x01010101, sum);
@@ -392,7 +412,7 @@ template <bool VEC>
 __device__ __forceinline__ void put_codes(int8_t* q, int c, int d, const float (&v)[8],
                                           const TokenScale& ts, int& sum) {
   uint2 w = make_uint2(0u, 0u);
-  if (!ts.zero) w = quant8(v, ts.s, ts.inv_s, sum);
+  if (!ts.zero) w = quant8(v, 1.f, ts.s, ts.inv_s, sum);
   if (VEC || 8 * c + 8 <= d) {
     *reinterpret_cast<uint2*>(q + 8 * c) = w;
   } else {
@@ -416,50 +436,177 @@ __device__ __forceinline__ void token_out(const QuantArgs& a, int64_t t, float s
   }
 }
 
-// Tokens whose Hadamard blocks are above 8: one CTA per token, which holds the row in shared memory.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(TQ_MAX_THREADS, TQ_CTAS) quant_rotated_kernel(QuantArgs a) {
-  extern __shared__ float xs[];
-  __shared__ uint32_t red_max[TQ_MAX_THREADS / 32];
-  __shared__ int red_sum[TQ_MAX_THREADS / 32];
-  const int64_t t = blockIdx.x;
-  const T* x = static_cast<const T*>(a.x) + t * a.ld_x;
-  const int units = a.d >> 3;
-  tq_wait();                       // x may come from the kernel before
-  if (a.chained) tq_launch_next();
-#pragma unroll 2
-  for (int c = threadIdx.x; c < units; c += blockDim.x) {
-    float v[8];
-    tq_load8<VEC>(x, 8 * c, a.d, v);
-    if (a.s_x) {
-      float s[8];
-      tq_load8<VEC>(a.s_x, 8 * c, a.d, s);
-      // the 2-ulp division: the rotation mixes entries whose roundings differ anyway
+// Four elements from j0 on. VEC: in one load.
+template <bool VEC>
+__device__ __forceinline__ float4 tq_load4(const float* p, int j0) {
+  if (VEC) return *reinterpret_cast<const float4*>(p + j0);
+  return make_float4(p[j0], p[j0 + 1], p[j0 + 2], p[j0 + 3]);
+}
+template <bool VEC>
+__device__ __forceinline__ uint32_t tq_signs4(const int8_t* p, int j0) {
+  if (VEC) return *reinterpret_cast<const uint32_t*>(p + j0);
+  uint32_t w = 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = tq_quotient(v[e], s[e]);
-    }
-    tq_signs8<VEC>(a.sign_in, 8 * c, a.d, v);
-    butterflies<8>(v, 8);
-    float* p = xs + tq_at(8 * c);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) p[e] = v[e];
+  for (int e = 0; e < 4; ++e) w |= (static_cast<uint32_t>(p[j0 + e]) & 0xffu) << (8 * e);
+  return w;
+}
+__device__ __forceinline__ float tq_signed(float v, uint32_t signs, int e) {
+  return __uint_as_float(__float_as_uint(v) ^ ((signs << (24 - 8 * e)) & 0x80000000u));
+}
+// Four signed elements.
+template <bool VEC>
+__device__ __forceinline__ float4 tq_load4(const float* p, int j0, uint32_t signs) {
+  const float4 v = tq_load4<VEC>(p, j0);
+  return make_float4(tq_signed(v.x, signs, 0), tq_signed(v.y, signs, 1), tq_signed(v.z, signs, 2),
+                     tq_signed(v.w, signs, 3));
+}
+template <bool VEC>
+__device__ __forceinline__ float4 tq_load4(const __nv_bfloat16* p, int j0, uint32_t signs) {
+  uint2 r;
+  if (VEC) {
+    r = *reinterpret_cast<const uint2*>(p + j0);
+  } else {
+    const uint16_t* h = reinterpret_cast<const uint16_t*>(p) + j0;
+    r = make_uint2(h[0] | (static_cast<uint32_t>(h[1]) << 16),
+                   h[2] | (static_cast<uint32_t>(h[3]) << 16));
   }
-  __syncthreads();
-  float amax = 0.f;
-  hadamard_passes(xs, a.d, a.log_b, amax);
-  const TokenScale ts = token_scale(__float_as_uint(amax * a.inv_sqrt_b) & 0x7fffffffu, red_max);
-  int sum = 0;
-  for (int c = threadIdx.x; c < units; c += blockDim.x) {
-    const float* p = xs + tq_at(8 * c);
-    float v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = p[e] * a.inv_sqrt_b;
-    put_codes<true>(a.q + t * a.ld_q, c, a.d, v, ts, sum);
-  }
-  token_out(a, t, ts.s, sum, red_sum);
+  r.x ^= __byte_perm(signs, 0u, 0x1404) & 0x80008000u;   // two sign bits at once
+  r.y ^= __byte_perm(signs, 0u, 0x3424) & 0x80008000u;
+  return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u),
+                     __uint_as_float(r.y << 16), __uint_as_float(r.y & 0xffff0000u));
 }
 
-// Tokens without a rotation, or with blocks of at most 8: one CTA per token. A thread keeps its first
+// Tokens whose Hadamard blocks are above 8: one CTA per token, which holds the row in shared memory.
+// Bound by instructions (35 per element, 57 % of the issue slots): 2048 x 8192 bf16 in 34 us, 1.5 TB/s.
+// With 8 neighbours a thread and four passes it took 38.5 us.
+template <typename T, bool VEC, int TOP>
+__global__ void __launch_bounds__(TQ_MAX_THREADS, TQ_CTAS) quant_rotated_kernel(QuantArgs a) {
+  extern __shared__ __align__(16) float xs[];
+  __shared__ uint32_t red_max[TQ_MAX_THREADS / 32];
+  __shared__ int red_sum[TQ_MAX_THREADS / 32];
+  constexpr int G = 1 << TOP;      // groups that meet in a thread
+  constexpr int U = 8 / G;         // sets of them under way together
+  const int64_t t = blockIdx.x;
+  const T* x = static_cast<const T*>(a.x) + t * a.ld_x;
+  const int tid = threadIdx.x, nthr = blockDim.x;
+  tq_wait();                       // x may come from the kernel before
+  if (a.chained) tq_launch_next();
+  const int log_step = a.log_b - TOP - 2, sets = a.d >> (TOP + 2);
+  for (int w0 = tid; w0 < sets; w0 += U * nthr) {
+    float4 v[U][G];
+    int g0[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int w = min(w0 + u * nthr, sets - 1);
+      g0[u] = (w & ((1 << log_step) - 1)) | ((w >> log_step) << (log_step + TOP));
+#pragma unroll
+      for (int j = 0; j < G; ++j) {
+        const int j0 = 4 * (g0[u] + (j << log_step));
+        v[u][j] = tq_load4<VEC>(x, j0, tq_signs4<VEC>(a.sign_in, j0));
+      }
+    }
+    if (a.s_x) {
+      // the 2-ulp division: the rotation mixes entries whose roundings differ anyway
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < G; ++j) {
+          const float4 s = tq_load4<VEC>(a.s_x, 4 * (g0[u] + (j << log_step)));
+          v[u][j] = make_float4(tq_quotient(v[u][j].x, s.x), tq_quotient(v[u][j].y, s.y),
+                                tq_quotient(v[u][j].z, s.z), tq_quotient(v[u][j].w, s.w));
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float e[4 * G];
+#pragma unroll
+      for (int j = 0; j < G; ++j) {
+        e[4 * j] = v[u][j].x;
+        e[4 * j + 1] = v[u][j].y;
+        e[4 * j + 2] = v[u][j].z;
+        e[4 * j + 3] = v[u][j].w;
+      }
+      butterflies<4 * G>(e, 4 * G);
+      if (w0 + u * nthr < sets) {
+#pragma unroll
+        for (int j = 0; j < G; ++j)
+          *tq_group(xs, g0[u] + (j << log_step)) =
+              make_ulonglong2(tq_pack2(e[4 * j], e[4 * j + 1]), tq_pack2(e[4 * j + 2], e[4 * j + 3]));
+      }
+    }
+  }
+  const int strips = (a.d + 31) >> 5;
+  if ((a.d & 31) && tid < 4)       // blocks of 16: the last strip's other half
+    *tq_group(xs, (a.d >> 2) + tid) = make_ulonglong2(0, 0);
+  __syncthreads();
+  columns(xs, a.d, a.log_b);
+  middle_bits(xs, a.d, a.log_b);
+  float amax = 0.f;
+  int sum = 0;
+  int8_t* q = a.q + t * a.ld_q;
+  auto last_stages = [&](uint64_t (&p)[16]) {
+    pair_stages(p, 2, 8);          // bits 2, 3
+    if (a.log_b > 4) pair_stages(p, 8, 16);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float2 f = tq_unpack2(p[i]);
+      amax = max_abs(max_abs(amax, f.x), f.y);
+    }
+  };
+  auto codes = [&](int c, const uint64_t (&p)[16], const TokenScale& ts) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (32 * c + 16 * h >= a.d) break;
+      uint2 w[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = tq_unpack2(p[8 * h + 4 * i + k]);
+          v[2 * k] = f.x;
+          v[2 * k + 1] = f.y;
+        }
+        w[i] = make_uint2(0u, 0u);
+        if (!ts.zero) w[i] = quant8(v, a.inv_sqrt_b, ts.s, ts.inv_s, sum);
+      }
+      *reinterpret_cast<uint4*>(q + 32 * c + 16 * h) = make_uint4(w[0].x, w[0].y, w[1].x, w[1].y);
+    }
+  };
+  auto scale = [&]() {
+    return token_scale(__float_as_uint(amax * a.inv_sqrt_b) & 0x7fffffffu, red_max);
+  };
+  float s;
+  if (strips <= nthr) {
+    uint64_t p[16];
+    if (tid < strips) {
+      strip_get(xs, tid, p);
+      last_stages(p);
+    }
+    const TokenScale ts = scale();
+    if (tid < strips) codes(tid, p, ts);
+    s = ts.s;
+  } else {
+    for (int c = tid; c < strips; c += nthr) {
+      uint64_t p[16];
+      strip_get(xs, c, p);
+      last_stages(p);
+      strip_put(xs, c, p);
+    }
+    const TokenScale ts = scale();
+    for (int c = tid; c < strips; c += nthr) {
+      uint64_t p[16];
+      strip_get(xs, c, p);
+      codes(c, p, ts);
+    }
+    s = ts.s;
+  }
+  token_out(a, t, s, sum, red_sum);
+}
+
+// Tokens without a rotation, or with blocks of at most 8: one CTA per token. 4096 x 11000 bf16 in 38 us
+// (3.6 TB/s; the floor is 21), half of the issue slots used: the row's latency, the maximum between two
+// passes over its registers, is what is left. A version without held registers read the row twice, 47 us. A thread keeps its first
 // TQ_HOLD units as they came (all of them up to a width of 12288) and reads others again.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(TQ_THREADS, 4) quant_plain_kernel(QuantArgs a) {
@@ -542,9 +689,68 @@ struct OutArgs {
   int64_t ld_y;
 };
 
-// One CTA per (token, span of whole Hadamard blocks).
+// The output kernels start while the product still runs: what they read last comes to L2 meanwhile.
+__device__ __forceinline__ void prefetch_channels(const OutArgs& a, int j0, int len) {
+  for (int c = 32 * threadIdx.x; c < len; c += 32 * blockDim.x) {
+    if (a.s_g) tq_prefetch(a.s_g + j0 + c);
+    if ((c & 127) == 0) tq_prefetch(a.sign_out + j0 + c);
+  }
+}
+
+// Element i of a row in shared memory sits at i + i / 32: the 8 consecutive elements of 32 threads,
+// and 32 consecutive elements, lie in different banks.
+__device__ __forceinline__ int units_at(int i) { return i + (i >> 5); }
+
+// Stages of the index bits [SH, SH + R) of len elements (a multiple of 2^(SH + R)).
+template <int R, int SH>
+__device__ __forceinline__ void unit_pass(float* xs, int len) {
+  constexpr int N = 1 << R;
+  // In the first pass (SH = 3) eight threads share the low bits; four groups of them would meet in
+  // the same banks 2^(3 + R) apart, and do not 256 apart: the bits of w above 3 that a warp counts
+  // through become index bits 8 and 9.
+  constexpr int B8 = SH == 3 ? 5 - R : 0;            // bits between 3 + R and 8
+  const bool spread = SH == 3 && (len & 1023) == 0;
+  for (int w = threadIdx.x; w < (len >> R); w += blockDim.x) {
+    int hi = w >> SH;
+    if (spread)
+      hi = (hi & ~((4 << B8) - 1)) | ((hi & 3) << B8) | ((hi >> 2) & ((1 << B8) - 1));
+    float* const p = xs + units_at((w & ((1 << SH) - 1)) | (hi << (SH + R)));
+    // units_at of 2^SH j past it (for SH = 3 its low five bits are below 8)
+    auto off = [](int j) { return (j << SH) + ((j << SH) >> 5); };
+    float v[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = p[off(j)];
+    butterflies<N>(v, N);
+#pragma unroll
+    for (int j = 0; j < N; ++j) p[off(j)] = v[j];
+  }
+  __syncthreads();
+}
+
+// The stages above the first three of every block of 2^L (3 < L <= 10). Written out per L, so that
+// every offset is a constant of its instruction.
+__device__ __forceinline__ void unit_passes(float* xs, int len, int L) {
+  switch (L) {
+    case 4: unit_pass<1, 3>(xs, len); break;
+    case 5: unit_pass<2, 3>(xs, len); break;
+    case 6: unit_pass<3, 3>(xs, len); break;
+    case 7: unit_pass<4, 3>(xs, len); break;
+    case 10:
+      unit_pass<4, 3>(xs, len);
+      unit_pass<3, 7>(xs, len);
+      break;
+    default:
+      unit_pass<3, 3>(xs, len);
+      if (L == 8) unit_pass<2, 6>(xs, len);
+      else unit_pass<3, 6>(xs, len);
+  }
+}
+
+// Blocks up to 1024. One CTA per (token, span of whole blocks). A thread takes units of 8 neighbours
+// (their three stages in registers), the other stages go through shared memory in one or two passes of
+// up to 16 elements a thread.
 template <typename Y, bool VEC>
-__global__ void __launch_bounds__(TQ_MAX_THREADS, TQ_CTAS) out_transform_kernel(OutArgs a) {
+__global__ void __launch_bounds__(UNIT_THREADS, 3) out_units_kernel(OutArgs a) {
   extern __shared__ float xs[];
   const int64_t t = blockIdx.y;
   const int j0 = blockIdx.x * a.span;
@@ -565,6 +771,7 @@ __global__ void __launch_bounds__(TQ_MAX_THREADS, TQ_CTAS) out_transform_kernel(
     }
     tq_store8<VEC>(y, 8 * c, len, v);
   };
+  prefetch_channels(a, j0, len);
   tq_wait();
   if (a.b <= 8) {
     for (int c = threadIdx.x; c < units; c += blockDim.x) {
@@ -580,15 +787,14 @@ __global__ void __launch_bounds__(TQ_MAX_THREADS, TQ_CTAS) out_transform_kernel(
     float v[8];
     tq_load8<VEC>(yp, 8 * c, len, v);
     butterflies<8>(v, 8);
-    float* p = xs + tq_at(8 * c);
+    float* p = xs + units_at(8 * c);
 #pragma unroll
     for (int e = 0; e < 8; ++e) p[e] = v[e];
   }
   __syncthreads();
-  float unused = 0.f;
-  hadamard_passes(xs, len, a.log_b, unused);
+  unit_passes(xs, len, a.log_b);
   for (int c = threadIdx.x; c < units; c += blockDim.x) {
-    const float* p = xs + tq_at(8 * c);
+    const float* p = xs + units_at(8 * c);
     float v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = p[e];
@@ -596,11 +802,109 @@ __global__ void __launch_bounds__(TQ_MAX_THREADS, TQ_CTAS) out_transform_kernel(
   }
 }
 
+template <bool VEC>
+__device__ __forceinline__ void tq_store4(float* p, int j0, const float (&v)[4]) {
+  if (VEC) {
+    *reinterpret_cast<float4*>(p + j0) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) p[j0 + e] = v[e];
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void tq_store4(__nv_bfloat16* p, int j0, const float (&v)[4]) {
+  if (VEC) {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
+    *reinterpret_cast<uint2*>(p + j0) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                                   *reinterpret_cast<const uint32_t*>(&hi));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) p[j0 + e] = __float2bfloat16_rn(v[e]);
+  }
+}
+
+// Blocks of 2048 and more. One CTA per (token, span of whole blocks): columns, strips, groups.
+template <typename Y, bool VEC, int TOP>
+__global__ void __launch_bounds__(TQ_MAX_THREADS, TQ_CTAS)
+    out_transform_kernel(OutArgs a) {
+  extern __shared__ __align__(16) float xs[];
+  constexpr int G = 1 << TOP, U = 8 / G;
+  const int64_t t = blockIdx.y;
+  const int j0 = blockIdx.x * a.span;
+  const int len = min(a.span, a.d - j0);
+  const int tid = threadIdx.x, nthr = blockDim.x;
+  Y* y = static_cast<Y*>(a.y) + t * a.ld_y + j0;
+  prefetch_channels(a, j0, len);
+  tq_wait();
+  column_pass<5, 5, true>(xs, a.yp + t * a.ld_yp + j0, len);
+  for (int c = tid; c < len >> 5; c += nthr) {
+    uint64_t p[16];
+    strip_get(xs, c, p);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float2 f = tq_unpack2(p[i]);
+      p[i] = tq_pack2(f.x + f.y, f.x - f.y);
+    }
+    pair_stages(p, 1, 16);
+    strip_put(xs, c, p);
+  }
+  __syncthreads();
+  middle_bits(xs, len, a.log_b);
+  const int log_step = a.log_b - TOP - 2, sets = len >> (TOP + 2);
+  const float* s_g = a.s_g ? a.s_g + j0 : nullptr;
+  for (int w0 = tid; w0 < sets; w0 += U * nthr) {
+    uint64_t p[U][2 * G];
+    uint32_t sg[U][G];
+    int g0[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int w = min(w0 + u * nthr, sets - 1);
+      g0[u] = (w & ((1 << log_step) - 1)) | ((w >> log_step) << (log_step + TOP));
+#pragma unroll
+      for (int j = 0; j < G; ++j) {
+        const int g = g0[u] + (j << log_step);
+        sg[u][j] = tq_signs4<VEC>(a.sign_out + j0, 4 * g);
+        const ulonglong2 r = *tq_group(xs, g);
+        p[u][2 * j] = r.x;
+        p[u][2 * j + 1] = r.y;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (w0 + u * nthr >= sets) break;
+      pair_stages(p[u], 2, 2 * G);
+#pragma unroll
+      for (int j = 0; j < G; ++j) {
+        const float2 lo = tq_unpack2(p[u][2 * j]), hi = tq_unpack2(p[u][2 * j + 1]);
+        float v[4] = {lo.x, lo.y, hi.x, hi.y};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = tq_signed(v[e] * a.inv_sqrt_b, sg[u][j], e);
+        const int c0 = 4 * (g0[u] + (j << log_step));
+        if (s_g) {
+          const float4 s = tq_load4<VEC>(s_g, c0);
+          v[0] = tq_quotient(v[0], s.x);
+          v[1] = tq_quotient(v[1], s.y);
+          v[2] = tq_quotient(v[2], s.z);
+          v[3] = tq_quotient(v[3], s.w);
+        }
+        tq_store4<VEC>(y, c0, v);
+      }
+    }
+  }
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 // threads for `units` units of 8: two a thread, evenly
 int unit_threads(int units) {
-  const int per = std::max(2, (units + TQ_MAX_THREADS - 1) / TQ_MAX_THREADS);
+  const int per = std::max(2, (units + UNIT_THREADS - 1) / UNIT_THREADS);
   return std::max(32, ((units + per - 1) / per + 31) / 32 * 32);
+}
+size_t unit_smem(int len) { return static_cast<size_t>(33) * ((len + 31) / 32) * sizeof(float); }
+// threads for a row of len elements: a strip each, or several, evenly
+int row_threads(int len) {
+  const int strips = (len + 31) / 32;
+  const int per = (strips + TQ_MAX_THREADS - 1) / TQ_MAX_THREADS;
+  return ((strips + per - 1) / per + 31) / 32 * 32;
 }
 int pow2_part(int d) { return d & (-d); }
 int log2_of(int b) {
@@ -608,7 +912,7 @@ int log2_of(int b) {
   while ((1 << l) < b) ++l;
   return l;
 }
-size_t row_smem(int len) { return static_cast<size_t>(33) * ((len + 31) / 32) * sizeof(float); }   // tq_at
+size_t row_smem(int len) { return static_cast<size_t>((len + 31) / 32) * 32 * sizeof(float); }
 
 }  // namespace
 
@@ -633,7 +937,7 @@ kronq_status run_quant_tokens(const QuantTokensArgs& q, cudaStream_t stream) {
                    aligned16(q.s_x) && aligned16(q.sign_in);
   const int units = (q.d + 7) / 8;
   // unrotated: two units a thread as far as TQ_THREADS go
-  const int threads = smem_row ? unit_threads(units)
+  const int threads = smem_row ? row_threads(q.d)
                                : std::min(TQ_THREADS, std::max(32, ((units + 1) / 2 + 31) / 32 * 32));
   auto launch = [&](auto kern) -> kronq_status {
     if (smem > 48 * 1024)
@@ -644,7 +948,12 @@ kronq_status run_quant_tokens(const QuantTokensArgs& q, cudaStream_t stream) {
   auto typed = [&](auto x) -> kronq_status {
     using T = decltype(x);
     if (smem_row)
-      return vec ? launch(quant_rotated_kernel<T, true>) : launch(quant_rotated_kernel<T, false>);
+      switch (top_bits(a.log_b)) {
+        case 0: return vec ? launch(quant_rotated_kernel<T, true, 0>) : launch(quant_rotated_kernel<T, false, 0>);
+        case 1: return vec ? launch(quant_rotated_kernel<T, true, 1>) : launch(quant_rotated_kernel<T, false, 1>);
+        case 2: return vec ? launch(quant_rotated_kernel<T, true, 2>) : launch(quant_rotated_kernel<T, false, 2>);
+        default: return vec ? launch(quant_rotated_kernel<T, true, 3>) : launch(quant_rotated_kernel<T, false, 3>);
+      }
     return vec ? launch(quant_plain_kernel<T, true>) : launch(quant_plain_kernel<T, false>);
   };
   return q.x_dtype == KRONQ_DTYPE_BF16 ? typed(__nv_bfloat16()) : typed(0.f);
@@ -666,21 +975,31 @@ kronq_status run_out_transform(const float* yp, int64_t ld_yp, int n, int d, con
   a.inv_sqrt_b = static_cast<float>(1.0 / std::sqrt(static_cast<double>(a.b)));
   a.y = y;
   a.ld_y = ld_y;
-  const size_t smem = a.b > 8 ? row_smem(a.span) : 0;
   const bool vec = d % 8 == 0 && aligned16(yp) && ld_yp % 4 == 0 && aligned16(y) &&
                    (n == 1 || ld_y % 8 == 0) && aligned16(s_g) && aligned16(sign_out);
   const dim3 grid((d + a.span - 1) / a.span, n);
+  // The kernel goes by the block alone, so that a token's bits do not depend on the batch. Either side,
+  // us a layer (d_out x d_in, tokens; units / strips): 11008 x 4096, 1: 17.9 / 19.5, 2048: 122 / 121;
+  // 8192 x 8192, 1: 22.8 / 21.7, 2048: 173 / 161; 28672 x 8192, 8: 53.7 / 55.8, 2048: 460 / 435.
+  const bool units = a.b <= 1024;
+  const int threads = units ? unit_threads(a.span / 8) : row_threads(a.span);
+  const size_t smem = a.b <= 8 ? 0 : units ? unit_smem(a.span) : row_smem(a.span);
   auto launch = [&](auto kern) -> kronq_status {
     if (smem > 48 * 1024)
       KQ_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem)));
-    return launch_chained(kern, grid, dim3(unit_threads(a.span / 8)), smem, stream, 1,
-                          "out_transform_kernel", a);
+    return launch_chained(kern, grid, dim3(threads), smem, stream, 1, "output transform kernel", a);
   };
-  if (y_dtype == KRONQ_DTYPE_BF16)
-    return vec ? launch(out_transform_kernel<__nv_bfloat16, true>)
-               : launch(out_transform_kernel<__nv_bfloat16, false>);
-  return vec ? launch(out_transform_kernel<float, true>) : launch(out_transform_kernel<float, false>);
+  auto typed = [&](auto out) -> kronq_status {
+    using Y = decltype(out);
+    if (units) return vec ? launch(out_units_kernel<Y, true>) : launch(out_units_kernel<Y, false>);
+    switch (top_bits(a.log_b)) {
+      case 1: return vec ? launch(out_transform_kernel<Y, true, 1>) : launch(out_transform_kernel<Y, false, 1>);
+      case 2: return vec ? launch(out_transform_kernel<Y, true, 2>) : launch(out_transform_kernel<Y, false, 2>);
+      default: return vec ? launch(out_transform_kernel<Y, true, 3>) : launch(out_transform_kernel<Y, false, 3>);
+    }
+  };
+  return y_dtype == KRONQ_DTYPE_BF16 ? typed(__nv_bfloat16()) : typed(0.f);
 }
 
 }  // namespace kq

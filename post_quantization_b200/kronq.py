@@ -8,6 +8,7 @@ raises (build it with `python -m post_quantization_b200.build`).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -476,6 +477,16 @@ def kronq_qlinear(x, packed, packed_grid, s_x, s_g, sign_in, sign_out, flags, d_
     _check(st, "kronq_qlinear")
 
 
+def on_stream(stream, device):
+    """The context in which torch allocates for a launch on `stream` (None: the current one), so that
+    the memory is not handed on while that stream still uses it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
 # ------------------------------------------------------------------------------ 7. 8-bit layer
 
 def kronq_quantize_tokens(x, q, tok_scale, tok_sum, s_x=None, sign_in=None, flags=0, stream=None):
@@ -542,8 +553,9 @@ def kronq_qlinear8(x, codes, scale, zero, s_x, s_g, sign_in, sign_out, flags, y,
                          ("s_x", s_x, torch.float32, d_in), ("s_g", s_g, torch.float32, d_out),
                          ("sign_in", sign_in, torch.int8, d_in),
                          ("sign_out", sign_out, torch.int8, d_out)))
-    ws, wsb = _workspace(lib.kronq_qlinear8_workspace_size(n_tok, d_out, d_in, int(flags)),
-                         x.device, workspace)
+    size = lib.kronq_qlinear8_workspace_size(n_tok, d_out, d_in, int(flags))
+    with on_stream(stream if workspace is None else None, x.device):
+        ws, wsb = _workspace(size, x.device, workspace)
     _check(lib.kronq_qlinear8(_p(x), xd, ld_x, n_tok, _p(codes), cd, ld_codes, _p(scale), _p(zero),
                               _p(s_x), _p(s_g), _p(sign_in), _p(sign_out), int(flags), d_out, d_in,
                               _p(y), yd, ld_y, _p(ws), wsb, st), "kronq_qlinear8")

@@ -153,14 +153,16 @@ class Linear8:
         return cls(r.codes, r.scale, r.zero, r.s_x, r.s_g, sign_in, sign_out)
 
     def __call__(self, x, y=None, dtype=torch.bfloat16, ws=None, stream=None):
-        """x: n_tok x d_in (bf16 or fp32). Returns y (n_tok x d_out, `dtype` unless given)."""
+        """x: n_tok x d_in (bf16 or fp32). Returns y (n_tok x d_out, `dtype` unless given; it belongs
+        to `stream`, on which the call runs)."""
         d_out, d_in = self.codes.shape
-        if y is None:
-            y = torch.empty(x.shape[0], d_out, dtype=dtype, device=x.device)
         wsz = K.kronq_qlinear8_workspace_size(x.shape[0], d_out, d_in, self.flags)
+        with K.on_stream(stream, x.device):
+            if y is None:
+                y = torch.empty(x.shape[0], d_out, dtype=dtype, device=x.device)
+            work = ws.get(wsz) if ws is not None else None
         K.kronq_qlinear8(x, self.codes, self.scale, self.zero, self.s_x, self.s_g, self.sign_in,
-                         self.sign_out, self.flags, y,
-                         workspace=ws.get(wsz) if ws is not None else None, stream=stream)
+                         self.sign_out, self.flags, y, workspace=work, stream=stream)
         return y
 
 

@@ -382,3 +382,119 @@ def test_matmul_i8_prompts(K, n, d_out, d_in, signed):
         tol = (3.1 * U32 + HALF[dtype]) * want.abs() + 1e-300
         assert bool(((y.double() - want).abs() <= tol).all())
     assert K.kronq_device_error() == 0
+
+
+@pytest.mark.parametrize("d", [16, 48, 96, 192, 384, 1536, 2048, 6144, 32768, 49152])
+def test_rotations_of_every_block_size(K, d):
+    """Blocks of 16 .. 32768 on both sides, on aligned rows and on others: the same bits."""
+    n, d2 = 3, min(d, 16384)
+    tag = ("i8b", d)
+    x = synth.activations(n, d, synth.seed_for(tag), dtype=torch.bfloat16, device="cuda")
+    si = synth.rademacher(d, synth.seed_for(tag, "si"), device="cuda")
+    s_x = synth.positive_scales(d, synth.seed_for(tag, "s"), device="cuda")
+    q, scale, total = quantize(K, x, s_x, si)
+    xp, s, _, _ = O.quantize_tokens(np64(x), np64(s_x), np64(si))
+    b = O.hadamard_block_size(d)
+    mag = np.abs(np64(x) / np64(s_x)).reshape(n, d // b, b).sum(-1) / math.sqrt(b)
+    err = (math.log2(b) + 4) * U32 * mag
+    assert (np.abs(np64(scale) - s) <= err.max(1) / 127 + 2 * U32 * s).all()
+    off = np.abs(q.cpu().numpy() - xp / np64(scale)[:, None])
+    assert (off <= 0.5 + np.repeat(err, b, axis=1) / np64(scale)[:, None] + 1e-12).all()
+    np.testing.assert_array_equal(total.cpu().numpy(), q.cpu().numpy().astype(np.int64).sum(1))
+    for dtype in (torch.bfloat16, torch.float32):      # rows off alignment; fp32 holds the same x
+        xo = torch.zeros(n, d + 3, dtype=dtype, device="cuda")[:, 1:d + 1]
+        xo.copy_(x)
+        qo, so, to = quantize(K, xo, s_x, si)
+        assert torch.equal(q, qo) and torch.equal(scale, so) and torch.equal(total, to)
+
+    codes, ws, zero = weights(d2, 64, False, tag)
+    x2 = synth.activations(n, 64, synth.seed_for(tag, "x"), dtype=torch.bfloat16, device="cuda")
+    s_g = synth.positive_scales(d2, synth.seed_for(tag, "sg"), device="cuda")
+    sgn = synth.rademacher(d2, synth.seed_for(tag, "so"), device="cuda")
+    flags = K.BIIP_SCALE_OUT | K.BIIP_ROTATE_OUT
+    q, ts, _ = quantize(K, x2)
+    yp = O.matmul_i8(q.cpu().numpy(), np64(ts), codes.cpu().numpy(), np64(ws), np64(zero))
+    want = O.hadamard_rows(yp) * np64(sgn)[None, :] / np64(s_g)[None, :]
+    b = O.hadamard_block_size(d2)
+    mag = np.repeat(np.abs(yp).reshape(n, d2 // b, b).sum(-1) / math.sqrt(b), b, axis=1) / np64(s_g)
+    for dtype in (torch.bfloat16, torch.float32):
+        y = torch.empty(n, d2, dtype=dtype, device="cuda")
+        yo = torch.full((n, d2 + 3), -7.0, dtype=dtype, device="cuda")
+        K.kronq_qlinear8(x2, codes, ws, zero, None, s_g, None, sgn, flags, y)
+        K.kronq_qlinear8(x2, codes, ws, zero, None, s_g, None, sgn, flags, yo[:, 1:d2 + 1])
+        torch.cuda.synchronize()
+        tol = (3.1 + math.log2(b) + 4) * U32 * mag + HALF[dtype] * np.abs(want)
+        assert (np.abs(np64(y) - want) <= tol).all()
+        assert torch.equal(y, yo[:, 1:d2 + 1])
+        assert bool((yo[:, 0] == -7.0).all()) and bool((yo[:, d2 + 1:] == -7.0).all())
+
+
+def test_rotated_tokens_that_are_not_finite(K):
+    """Infinities, NaN and sums past fp32 anywhere in a block: the token has no codes and scale NaN."""
+    d = 512
+    x = torch.randn(9, d, device="cuda")
+    si = torch.ones(d, dtype=torch.int8, device="cuda")
+    x[1] = 0.0
+    x[2, 77] = float("inf")
+    x[3, 300] = float("-inf")
+    x[3, 301] = float("inf")
+    x[4, 511] = float("nan")
+    x[5] = 0.0                                         # sums of 6e38, some of which cancel
+    x[5, [8, 9, 12]] = 3e38
+    x[5, [13]] = 3e38
+    x[6] = 0.0
+    x[6, [8, 9, 12, 13]] = torch.tensor([3e38, 3e38, -3e38, -3e38], device="cuda")
+    x[7] *= 1e-41
+    q, scale, total = quantize(K, x, None, si)
+    bad = torch.isnan(scale).tolist()
+    assert bad == [False, False, True, True, True, True, True, False, False]
+    rows = [1, 2, 3, 4, 5, 6, 7]
+    assert float(scale[1]) == 1.0 and float(scale[7]) == 1.0
+    assert int(q[rows].abs().max()) == 0 and int(total[rows].abs().max()) == 0
+    # the other rows do not feel them
+    ok, s_ok, _ = quantize(K, x[[0, 8]].contiguous(), None, si)
+    assert torch.equal(q[[0, 8]], ok) and torch.equal(scale[[0, 8]], s_ok)
+
+
+def test_two_streams_at_once(K):
+    """Tokens quantized and multiplied on two streams side by side, and codes that the call before
+    has just written: the bits of one call after the other."""
+    n, d_out, d_in = 200, 640, 1040
+    a = [weights(d_out, d_in, False, ("i8t", i)) for i in range(2)]
+    xs = [synth.activations(n, d_in, synth.seed_for(("i8t", "x"), i), dtype=torch.bfloat16,
+                            device="cuda") for i in range(2)]
+    si = synth.rademacher(d_in, 5, device="cuda")
+    so = synth.rademacher(d_out, 6, device="cuda")
+    want = []
+    for (c, s, z), x in zip(a, xs):
+        y = torch.empty(n, d_out, device="cuda")
+        K.kronq_qlinear8(x, c, s, z, None, None, si, so, K.BIIP_ROTATE_IN | K.BIIP_ROTATE_OUT, y)
+        want.append(y)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[torch.empty(n, d_out, device="cuda") for _ in range(6)] for _ in range(2)]
+    torch.cuda.synchronize()
+    for r in range(6):
+        for i, s in enumerate(streams):
+            c, sc, z = a[i]
+            K.kronq_qlinear8(xs[i], c, sc, z, None, None, si, so,
+                             K.BIIP_ROTATE_IN | K.BIIP_ROTATE_OUT, got[i][r], stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(w, g) for w, gs in zip(want, got) for g in gs)
+
+    # the codes themselves come from kronq_quantize_tokens (symmetric, one grid per row)
+    w = torch.randn(d_out, d_in, device="cuda")
+    codes = padded(d_out, d_in, torch.int8)
+    grid = torch.empty(d_out, device="cuda")
+    sums = torch.empty(d_out, dtype=torch.int32, device="cuda")
+    q, ts, total = quantize(K, xs[0])
+    y = torch.empty(n, d_out, device="cuda")
+    for k in range(4):
+        w.mul_(-1.25)
+        K.kronq_quantize_tokens(w, codes, grid, sums)
+        K.kronq_matmul_i8(q, ts, total, codes, grid, None, y)
+    torch.cuda.synchronize()
+    _, s, c, _ = O.quantize_tokens(w.cpu().numpy())
+    np.testing.assert_array_equal(codes.cpu().numpy(), c)
+    ref = O.matmul_i8(q.cpu().numpy(), np64(ts), c, s, None)
+    assert (np.abs(np64(y) - ref) <= 3.1 * 2 * U32 * np.abs(ref) + 1e-300).all()
