@@ -334,36 +334,61 @@ struct DsShared {
   int repeated;                  // an id is listed twice
 };
 
-// With a gradient, in dynamic shared memory: the list, and a table that finds out whether an id is
-// listed twice. Only then are the lists searched: the first j that lists an id adds up all its p,
-// in the order of the list.
+// With a gradient, in dynamic shared memory: the list, and a table of its ids. Of the entries with one
+// id the first stands for all; only where a row has such entries are lists searched, by a warp for each
+// repeated id, and their p added up in an order that the list alone fixes.
 struct IdTable {
+  static constexpr int SINGLE = 1 << 30;
   float* p;                      // k
   int* id;                       // k; -1: absent
-  int* slot;                     // hash_mask + 1: j of the entry that took the slot, or -1
+  int* slot;                     // hash_mask + 1: first entry with the slot's id, + SINGLE while it is
+                                 // the only one; -1: free
   __device__ __forceinline__ IdTable(const DsArgs& a, int* mem) {
     slot = mem;
     id = slot + a.hash_mask + 1;
     p = reinterpret_cast<float*>(id + a.k);
   }
+  __device__ __forceinline__ uint32_t start(const DsArgs& a, int j) const {
+    return (static_cast<uint32_t>(id[j]) * 2654435761u >> 16) & a.hash_mask;
+  }
   // Enters entry j; true where its id was there already. Every id[] is written before.
   __device__ __forceinline__ bool insert(const DsArgs& a, int j) const {
-    uint32_t h = (static_cast<uint32_t>(id[j]) * 2654435761u >> 16) & a.hash_mask;
+    uint32_t h = start(a, j);
     while (true) {               // at most k of >= 2 k slots are taken
-      const int old = atomicCAS(&slot[h], -1, j);
+      const int old = atomicCAS(&slot[h], -1, j + SINGLE);
       if (old == -1) return false;
-      if (id[old] == id[j]) return true;
+      const int first = old & (SINGLE - 1);
+      if (id[first] == id[j]) {  // a slot's entries may change, its id does not
+        atomicMin(&slot[h], min(first, j));
+        return true;
+      }
       h = (h + 1) & a.hash_mask;
     }
   }
-  // P of entry j's id, or -1 where an earlier entry lists it
-  __device__ __forceinline__ float total(const DsArgs& a, int j) const {
-    for (int l = 0; l < j; ++l)
-      if (id[l] == id[j]) return -1.f;
-    float sum = p[j];
-    for (int l = j + 1; l < a.k; ++l)
-      if (id[l] == id[j]) sum += p[l];
-    return sum;
+  // The slot of entry j, when all are entered
+  __device__ __forceinline__ int find(const DsArgs& a, int j) const {
+    uint32_t h = start(a, j);
+    while (id[slot[h] & (SINGLE - 1)] != id[j]) h = (h + 1) & a.hash_mask;
+    return slot[h];
+  }
+  // For a whole warp, one entry j a lane (mine: it asks). mine stays where j is its id's first entry;
+  // p becomes the sum over the id's entries.
+  __device__ __forceinline__ void join(const DsArgs& a, int j, bool& mine, float& pj) const {
+    const int at = mine ? find(a, j) : 0;
+    mine = mine && (at & (SINGLE - 1)) == j;
+    const int lane = threadIdx.x & 31;
+    unsigned todo = __ballot_sync(0xffffffffu, mine && !(at & SINGLE));
+    while (todo) {
+      const int from = __ffs(todo) - 1;
+      todo &= todo - 1;
+      const int want = id[__shfl_sync(0xffffffffu, j, from)];
+      float sum = 0.f;
+      for (int l = lane; l < a.k; l += 32)
+        if (id[l] == want) sum += p[l];
+#pragma unroll
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane == from) pj = sum;
+    }
   }
 };
 __host__ __device__ inline int id_table_words(const DsArgs& a) {
@@ -389,7 +414,7 @@ __device__ __forceinline__ void load_entries(const DsArgs& a, int64_t row, Entri
       const int64_t o = row * a.ld_top + j;
       const float t = a.top_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.top)[o])
                                  : static_cast<const float*>(a.top)[o];
-      if (id >= 0 && id < a.v) {
+      if (id >= 0 && id < a.v && t != kNegInf) {       // -inf counts nothing
         e.id[i] = id;
         e.t[i] = t;
       }
@@ -543,14 +568,14 @@ __device__ __forceinline__ void list_gradients(const DsArgs& a, const DsShared& 
     const int j = threadIdx.x + i * NT;
     patch_id[i] = -1;
     patch[i] = 0.f;
-    if (j < a.k && e.id[i] >= 0 && s.owns(e.id[i], part)) {
-      const float p = sh.repeated ? table.total(a, j) : e.p[i];
-      if (p >= 0.f || p != p) {
-        patch_id[i] = e.id[i];
-        if (wt != 0.f)
-          patch[i] = coef == 0.f ? -wt * p
-                                 : fmaf(coef, ex2(ds_exponent(e.z[i], rs.m, a.c)), -wt * p);
-      }
+    bool mine = j < a.k && e.id[i] >= 0 && s.owns(e.id[i], part);
+    float p = e.p[i];
+    if (sh.repeated) table.join(a, j, mine, p);
+    if (mine) {
+      patch_id[i] = e.id[i];
+      if (wt != 0.f)
+        patch[i] = coef == 0.f ? -wt * p
+                               : fmaf(coef, ex2(ds_exponent(e.z[i], rs.m, a.c)), -wt * p);
     }
   }
 }
@@ -737,7 +762,7 @@ __global__ void __launch_bounds__(DS_RING_THREADS, 2)
         }
 #pragma unroll
         for (int b = 0; b < B; ++b) {
-          if (id[b] < 0 || id[b] >= a.v) {
+          if (id[b] < 0 || id[b] >= a.v || x[b] == kNegInf) {   // -inf counts nothing
             id[b] = -1;
             x[b] = kNegInf;
           }
@@ -778,11 +803,14 @@ __global__ void __launch_bounds__(DS_RING_THREADS, 2)
         if (table.id[j] >= 0) again |= table.insert(a, j);
       again = __any_sync(0xffffffffu, again);
       if (again) {
-        for (int j = lane; j < a.k; j += 32) {
-          if (own[j] < 0) continue;
-          const float p = table.total(a, j);
-          if (p < 0.f) own[j] = -1;
-          grad[j] = p;
+        for (int j = lane; j - lane < a.k; j += 32) {
+          bool mine = j < a.k && own[j] >= 0;
+          float p = mine ? table.p[j] : 0.f;
+          table.join(a, j, mine, p);
+          if (j < a.k) {
+            if (!mine) own[j] = -1;
+            grad[j] = p;
+          }
         }
       }
       mbar_wait(&got[turn], parity, aborted, err, DEV_ERR_EPI_WAIT);

@@ -328,3 +328,28 @@ def test_many_long_rows(K, v, k, dtype):
         tol = (stat + 6 * 40 * U32) * (2 * unit * q + wg.abs()) + HALF[dtype] * wg.abs() + 1e-38
         assert bool(((dz[rows].double() - wg).abs() <= tol).all())
     assert K.kronq_device_error() == 0
+
+
+@pytest.mark.parametrize("n,v,k,dtype", [(3, 700, 300, torch.float32), (5, 50000, 1024, torch.bfloat16),
+                                         (320, 40000, 200, torch.bfloat16), (310, 40000, 1000, torch.float32)])
+def test_lists_that_repeat_their_ids(K, n, v, k, dtype):
+    """Many entries on few ids, one id for all, pads of -inf on one id: sums over the repeats."""
+    z, ids, t = inputs(n, v, k, dtype, 55)
+    r = np.random.default_rng(8)
+    ids.copy_(torch.from_numpy(r.integers(0, 5 * k, (n, k)).astype(np.int32) % v))
+    ids[0] = v - 1
+    ids[1, k // 3:] = 0
+    t[1, k // 3:] = float("-inf")
+    ids[2] = torch.arange(k, device="cuda", dtype=torch.int32).flip(0) // 2
+    w = torch.from_numpy(r.uniform(0.5, 2, n).astype(np.float32)).cuda()
+    loss, lse, dz = run(K, z, ids, t, 1.1, None, w)
+    again = run(K, z, ids, t, 1.1, None, w)
+    assert torch.equal(loss, again[0]) and torch.equal(lse, again[1]) and torch.equal(dz, again[2])
+    some = torch.tensor([0, 1, 2] + list(range(3, n, 37)))
+    check(z[some], ids[some], t[some], 1.1, None, w[some], loss[some], lse[some], dz[some])
+    back = torch.empty_like(dz)
+    K.kronq_distill_backward(z, ids, t, lse, w, back, temperature=1.1)
+    torch.cuda.synchronize()
+    check(z[some], ids[some], t[some], 1.1, None, w[some], None, None, back[some],
+          given_lse=lse[some])
+    assert K.kronq_device_error() == 0
