@@ -604,10 +604,11 @@ __global__ void __launch_bounds__(TQ_MAX_THREADS, TQ_CTAS) quant_rotated_kernel(
   token_out(a, t, s, sum, red_sum);
 }
 
-// Tokens without a rotation, or with blocks of at most 8: one CTA per token. 4096 x 11000 bf16 in 38 us
-// (3.6 TB/s; the floor is 21), half of the issue slots used: the row's latency, the maximum between two
-// passes over its registers, is what is left. A version without held registers read the row twice, 47 us. A thread keeps its first
+// Tokens without a rotation, or with blocks of at most 8: one CTA per token. A thread keeps its first
 // TQ_HOLD units as they came (all of them up to a width of 12288) and reads others again.
+// 4096 x 11000 bf16: 38 us, 3.6 TB/s, 46 % of the issue slots; the floor is 21 us. Each row waits for
+// its maximum between its loads and its stores, and four rows per SM do not hide all of that. Rounding
+// element by element (quant_code throughout) took 47 us.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(TQ_THREADS, 4) quant_plain_kernel(QuantArgs a) {
   __shared__ uint32_t red_max[TQ_THREADS / 32];
