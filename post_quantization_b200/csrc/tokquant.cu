@@ -94,10 +94,15 @@ struct Raw8<__nv_bfloat16> {
       r = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
   // the largest magnitude's bit pattern as fp32 (infinities and NaN come out largest)
   __device__ __forceinline__ uint32_t most() const {
     const uint32_t k = 0x7fff7fffu;
-    const uint32_t m = __vmaxu2(__vmaxu2(r.x & k, r.y & k), __vmaxu2(r.z & k, r.w & k));
+    const uint32_t m = max2(max2(r.x & k, r.y & k), max2(r.z & k, r.w & k));
     return max(m << 16, m & 0xffff0000u);
   }
   __device__ __forceinline__ void get(float (&v)[8]) const {
@@ -336,54 +341,44 @@ struct QuantArgs {
   int chained;             // the kernel behind it is the layer's product: let it start early
 };
 
-// rint(x / s) for |x| <= 127 s (1 + 2^-23) and a normal s, exactly as the real quotient rounds
-// (ties to even): the fp32 estimate is off by at most one, next to a border, and the remainder
-// x - q s is exact in fp32 there (it is a multiple of the smaller ulp and below 2^24 of them).
-__device__ __forceinline__ int quant_code(float x, float s, float inv_s) {
-  const float q0 = rintf(x * inv_s);
-  const float r = 2.f * fmaf(-q0, s, x);
-  float q = q0;
-  if (r > s || (r == s && (static_cast<int>(q0) & 1))) q += 1.f;
-  if (r < -s || (r == -s && (static_cast<int>(q0) & 1))) q -= 1.f;
-  return static_cast<int>(q);
-}
-
-// Eight codes as two words, of x = fl(v pre). x / s is estimated as v fl(pre inv_s), to 3 2^-17
-// absolute; adding 1.5 2^23 rounds it to an integer, whose low byte is the float's low byte. Where the
-// estimate lies within 10^-4 of a half (one thread in 600), the exact rounding takes over.
-__device__ __forceinline__ uint2 quant8(const float (&x)[8], float pre, float s, float inv_s,
-                                        int& sum) {
-  const float est = pre * inv_s;
+// Eight codes rint(x / s) (of the exact quotient, ties to even) as two words, for |x| <= 127 s
+// (1 + 2^-23) and a normal s. Adding 1.5 2^23 to x inv_s rounds it to an integer q, whose low byte is
+// the float's low byte. q is off by at most one, and only next to a half: there the remainder x - q s is
+// exact in fp32 (a multiple of the smaller ulp and below 2^24 of them), so that 2 |x - q s| against s
+// tells. (A test of the quotient's estimate instead sent most warps of bf16 tokens into the slow branch:
+// their values repeat, and so do those next to a half; 4096 x 11008 took 60 us.)
+__device__ __forceinline__ uint2 quant8(const float (&x)[8], float s, float inv_s, int& sum) {
   const uint64_t magic = tq_pack2(12582912.f, 12582912.f), unmagic = tq_pack2(-12582912.f, -12582912.f);
-  const uint64_t inv2 = tq_pack2(est, est), neg2 = tq_pack2(-est, -est);
-  uint32_t w[2];
+  const uint64_t inv2 = tq_pack2(inv_s, inv_s), neg2 = tq_pack2(-s, -s);
+  uint32_t t[8];
+  float r[8];
   float off = 0.f;
 #pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint64_t v = tq_pack2(x[2 * k], x[2 * k + 1]);
+    const uint64_t f = tq_fma2(v, inv2, magic);
+    const float2 d = tq_unpack2(tq_fma2(tq_add2(f, unmagic), neg2, v));     // x - q s
+    r[2 * k] = d.x;
+    r[2 * k + 1] = d.y;
+    off = fmaxf(off, fmaxf(fabsf(d.x), fabsf(d.y)));
+    const float2 b = tq_unpack2(f);
+    t[2 * k] = __float_as_uint(b.x);
+    t[2 * k + 1] = __float_as_uint(b.y);
+  }
+  if (off + off >= s) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float a = fabsf(r[k]) + fabsf(r[k]);
+      if (a > s || (a == s && (t[k] & 1u))) t[k] += r[k] > 0.f ? 1u : 0xffffffffu;
+    }
+  }
+  uint32_t w[2];
+#pragma unroll
   for (int i = 0; i < 2; ++i) {
-    uint32_t t[4];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const uint64_t v = tq_pack2(x[4 * i + 2 * k], x[4 * i + 2 * k + 1]);
-      const uint64_t f = tq_fma2(v, inv2, magic);
-      const float2 d = tq_unpack2(tq_fma2(v, neg2, tq_add2(f, unmagic)));   // -(x / s - q)
-      off = fmaxf(off, fmaxf(fabsf(d.x), fabsf(d.y)));
-      const float2 b = tq_unpack2(f);
-      t[2 * k] = __float_as_uint(b.x);
-      t[2 * k + 1] = __float_as_uint(b.y);
-    }
-    w[i] = __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
+    w[i] = __byte_perm(__byte_perm(t[4 * i], t[4 * i + 1], 0x0040),
+                       __byte_perm(t[4 * i + 2], t[4 * i + 3], 0x0040), 0x5410);
+    sum = __dp4a(static_cast<int>(w[i]), 0x01010101, sum);
   }
-  if (off > 0.4999f) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      w[i] = 0u;
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        w[i] |= (static_cast<uint32_t>(quant_code(x[4 * i + k] * pre, s, inv_s)) & 0xffu) << (8 * k);
-    }
-  }
-  sum = __dp4a(static_cast<int>(w[0]), 0x01010101, sum);
-  sum = __dp4a(static_cast<int>(w[1]), 0x01010101, sum);
   return make_uint2(w[0], w[1]);
 }
 
@@ -412,7 +407,7 @@ template <bool VEC>
 __device__ __forceinline__ void put_codes(int8_t* q, int c, int d, const float (&v)[8],
                                           const TokenScale& ts, int& sum) {
   uint2 w = make_uint2(0u, 0u);
-  if (!ts.zero) w = quant8(v, 1.f, ts.s, ts.inv_s, sum);
+  if (!ts.zero) w = quant8(v, ts.s, ts.inv_s, sum);
   if (VEC || 8 * c + 8 <= d) {
     *reinterpret_cast<uint2*>(q + 8 * c) = w;
   } else {
@@ -477,8 +472,8 @@ __device__ __forceinline__ float4 tq_load4(const __nv_bfloat16* p, int j0, uint3
 }
 
 // Tokens whose Hadamard blocks are above 8: one CTA per token, which holds the row in shared memory.
-// Bound by instructions (35 per element, 57 % of the issue slots): 2048 x 8192 bf16 in 34 us, 1.5 TB/s.
-// With 8 neighbours a thread and four passes it took 38.5 us.
+// Bound by instructions (about 33 a warp for 32 elements, 57 % of the issue slots): 2048 x 8192 bf16 in
+// 31 us, 1.6 TB/s. With 8 neighbours a thread and four passes it took 38.5 us.
 template <typename T, bool VEC, int TOP>
 __global__ void __launch_bounds__(TQ_MAX_THREADS, TQ_CTAS) quant_rotated_kernel(QuantArgs a) {
   extern __shared__ __align__(16) float xs[];
@@ -564,11 +559,11 @@ __global__ void __launch_bounds__(TQ_MAX_THREADS, TQ_CTAS) quant_rotated_kernel(
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const float2 f = tq_unpack2(p[8 * h + 4 * i + k]);
-          v[2 * k] = f.x;
-          v[2 * k + 1] = f.y;
+          v[2 * k] = f.x * a.inv_sqrt_b;
+          v[2 * k + 1] = f.y * a.inv_sqrt_b;
         }
         w[i] = make_uint2(0u, 0u);
-        if (!ts.zero) w[i] = quant8(v, a.inv_sqrt_b, ts.s, ts.inv_s, sum);
+        if (!ts.zero) w[i] = quant8(v, ts.s, ts.inv_s, sum);
       }
       *reinterpret_cast<uint4*>(q + 32 * c + 16 * h) = make_uint4(w[0].x, w[0].y, w[1].x, w[1].y);
     }
@@ -606,9 +601,9 @@ __global__ void __launch_bounds__(TQ_MAX_THREADS, TQ_CTAS) quant_rotated_kernel(
 
 // Tokens without a rotation, or with blocks of at most 8: one CTA per token. A thread keeps its first
 // TQ_HOLD units as they came (all of them up to a width of 12288) and reads others again.
-// 4096 x 11000 bf16: 38 us, 3.6 TB/s, 46 % of the issue slots; the floor is 21 us. Each row waits for
-// its maximum between its loads and its stores, and four rows per SM do not hide all of that. Rounding
-// element by element (quant_code throughout) took 47 us.
+// 4096 x 11008 bf16: 33 us, 4.1 TB/s, 57 % of the issue slots (fp32 43 us, 5.2 TB/s); the floor is 21
+// us. Each row waits for its maximum between its loads and its stores, and four rows per SM do not hide
+// all of that.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(TQ_THREADS, 4) quant_plain_kernel(QuantArgs a) {
   __shared__ uint32_t red_max[TQ_THREADS / 32];
