@@ -353,17 +353,21 @@ struct IdTable {
   }
   // Enters entry j; true where its id was there already. Every id[] is written before.
   __device__ __forceinline__ bool insert(const DsArgs& a, int j) const {
-    uint32_t h = start(a, j);
-    while (true) {               // at most k of >= 2 k slots are taken
-      const int old = atomicCAS(&slot[h], -1, j + SINGLE);
-      if (old == -1) return false;
+    const uint32_t h = start(a, j);
+    return settle(a, j, h, atomicCAS(&slot[h], -1, j + SINGLE));
+  }
+  // The rest of it, from what slot h held when entry j asked for it
+  __device__ __forceinline__ bool settle(const DsArgs& a, int j, uint32_t h, int old) const {
+    while (old != -1) {          // at most k of >= 2 k slots are taken
       const int first = old & (SINGLE - 1);
       if (id[first] == id[j]) {  // a slot's entries may change, its id does not
         atomicMin(&slot[h], min(first, j));
         return true;
       }
       h = (h + 1) & a.hash_mask;
+      old = atomicCAS(&slot[h], -1, j + SINGLE);
     }
+    return false;
   }
   // The slot of entry j, when all are entered
   __device__ __forceinline__ int find(const DsArgs& a, int j) const {
@@ -780,16 +784,32 @@ __global__ void __launch_bounds__(DS_RING_THREADS, 2)
           }
         }
       }
-      for (int j = lane; j < a.k; j += 32)            // a NaN logit makes s NaN
-        if (t[j] != kNegInf) ls.s += ex2(ds_exponent(t[j], ls.m == kNegInf ? 0.f : ls.m, a.c));
+      // the list is worked through B entries a lane at a time, whose steps overlap
+      const float lm = ls.m == kNegInf ? 0.f : ls.m;
+      for (int j0 = lane; j0 < a.k; j0 += 32 * B) {
+        float x[B];
+#pragma unroll
+        for (int b = 0; b < B; ++b) x[b] = j0 + 32 * b < a.k ? t[j0 + 32 * b] : kNegInf;
+#pragma unroll
+        for (int b = 0; b < B; ++b)                   // a NaN logit makes s NaN
+          if (x[b] != kNegInf) ls.s += ex2(ds_exponent(x[b], lm, a.c));
+      }
       ls = ds_join_lanes<32>(ls, a.c);
       // log p_j = t_j / tau - L_t in fp64: the difference of two numbers of the logits' size
       const double norm = a.top_lse ? static_cast<double>(a.top_lse[row]) : ds_lse(a, ls);
       float mass = 0.f;
-      for (int j = lane; j < a.k; j += 32) {
-        const float p = t[j] == kNegInf ? 0.f : expf(static_cast<float>(t[j] * a.inv_tau - norm));
-        table.p[j] = p;
-        mass += p;
+      for (int j0 = lane; j0 < a.k; j0 += 32 * B) {
+        float p[B];
+#pragma unroll
+        for (int b = 0; b < B; ++b) p[b] = j0 + 32 * b < a.k ? t[j0 + 32 * b] : kNegInf;
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+          p[b] = p[b] == kNegInf ? 0.f : expf(static_cast<float>(p[b] * a.inv_tau - norm));
+          mass += p[b];
+        }
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+          if (j0 + 32 * b < a.k) table.p[j0 + 32 * b] = p[b];
       }
 #pragma unroll
       for (int o = 16; o; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
@@ -799,8 +819,22 @@ __global__ void __launch_bounds__(DS_RING_THREADS, 2)
       }
       __syncwarp();
       bool again = false;
-      for (int j = lane; j < a.k; j += 32)
-        if (table.id[j] >= 0) again |= table.insert(a, j);
+      for (int j0 = lane; j0 < a.k; j0 += 32 * B) {
+        int old[B];
+        uint32_t h[B];
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+          const int j = j0 + 32 * b;
+          old[b] = -1;
+          if (j < a.k && table.id[j] >= 0) {
+            h[b] = table.start(a, j);
+            old[b] = atomicCAS(&table.slot[h[b]], -1, j + IdTable::SINGLE);
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+          if (old[b] != -1) again |= table.settle(a, j0 + 32 * b, h[b], old[b]);
+      }
       again = __any_sync(0xffffffffu, again);
       if (again) {
         for (int j = lane; j - lane < a.k; j += 32) {
@@ -818,20 +852,39 @@ __global__ void __launch_bounds__(DS_RING_THREADS, 2)
       __syncwarp();
       if (lane == 0) mbar_arrive(&taken[turn]);
       const float coef = ds_coef(wt, mass, rs.s);
-      for (int j = lane; j < a.k; j += 32) {
-        if (own[j] < 0) continue;
-        const float p = again ? grad[j] : table.p[j];
-        grad[j] = wt == 0.f ? 0.f
-                            : (coef == 0.f ? -wt * p
-                                           : fmaf(coef, ex2(ds_exponent(zk[j], rs.m, a.c)), -wt * p));
+      for (int j0 = lane; j0 < a.k; j0 += 32 * B) {
+        float p[B], z[B];
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+          const int j = min(j0 + 32 * b, a.k - 1);
+          p[b] = again ? grad[j] : table.p[j];
+          z[b] = zk[j];
+        }
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+          const float g = coef == 0.f ? -wt * p[b]
+                                      : fmaf(coef, ex2(ds_exponent(z[b], rs.m, a.c)), -wt * p[b]);
+          if (j0 + 32 * b < a.k) grad[j0 + 32 * b] = wt == 0.f ? 0.f : g;
+        }
       }
       if (part == 0) {
         const double lse = ds_lse(a, rs);
         double loss = 0.0;
-        for (int j = lane; j < a.k; j += 32)
-          if (table.p[j] != 0.f)                      // a masked listed entry: infinite loss
-            loss += zk[j] == kNegInf ? static_cast<double>(INFINITY)
-                                     : table.p[j] * ((static_cast<double>(t[j]) - zk[j]) * a.inv_tau - norm + lse);
+        for (int j0 = lane; j0 < a.k; j0 += 32 * B) {
+          float p[B], x[B], z[B];
+#pragma unroll
+          for (int b = 0; b < B; ++b) {
+            const int j = min(j0 + 32 * b, a.k - 1);
+            p[b] = j0 + 32 * b < a.k ? table.p[j] : 0.f;
+            x[b] = t[j];
+            z[b] = zk[j];
+          }
+#pragma unroll
+          for (int b = 0; b < B; ++b)
+            if (p[b] != 0.f)                          // a masked listed entry: infinite loss
+              loss += z[b] == kNegInf ? static_cast<double>(INFINITY)
+                                      : p[b] * ((static_cast<double>(x[b]) - z[b]) * a.inv_tau - norm + lse);
+        }
 #pragma unroll
         for (int o = 16; o; o >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, o);
         if (lane == 0) {
@@ -842,6 +895,7 @@ __global__ void __launch_bounds__(DS_RING_THREADS, 2)
       }
       mbar_wait(&stored[turn], parity, aborted, err, DEV_ERR_EPI_WAIT);
       D* dz = static_cast<D*>(a.dz) + row * a.ld_dz;
+#pragma unroll 4
       for (int j = lane; j < a.k; j += 32)
         if (own[j] >= 0) ds_st(dz + own[j], grad[j]);
       __syncwarp();
@@ -1172,16 +1226,28 @@ kronq_status launch_distill(DsArgs a, int n, bool lse, bool grad, cudaStream_t s
   }
   auto cut = [&] { return static_cast<int>((vecs + a.cl - 1) / a.cl); };
   if (grad) {
-    // Long rows, at least two per cluster: the fewest CTAs that hold a row with two chunks to spare
-    for (int ctas = 2; ctas >= 1 && vecs > DS_RING_MIN_VECS; --ctas) {
-      const int hold = ring_chunks(a, ctas) - 2;
-      a.cl = 1;
-      while (a.cl < DS_MAX_CL && vecs > static_cast<int64_t>(a.cl) * hold * DS_CHUNK_VECS)
-        a.cl *= 2;
+    // Long rows, at least two per cluster: the fewest CTAs that hold a row with two chunks to spare.
+    // Two CTAs per SM, unless the list takes so much of their memory that a row needs four times the
+    // CTAs, each of which works through the list (1024 rows, us with two and with one: 128256 wide,
+    // k = 128 (4 and 2 CTAs) 128 and 154, k = 256 (8 and 2) 208 and 158, k = 512 301 and 184; 50001
+    // wide, k = 256 (4 and 1) 99 and 78; 32000 wide, k = 256 (2 and 1) 56 and 60).
+    int cl[3] = {0, 0, 0};                       // by CTAs per SM; 0: a row does not fit
+    for (int ctas = 1; ctas <= 2; ++ctas) {
+      const int64_t hold = static_cast<int64_t>(ring_chunks(a, ctas) - 2) * DS_CHUNK_VECS;
+      for (int c = 1; c <= DS_MAX_CL && cl[ctas] == 0; c *= 2)
+        if ((vecs + c - 1) / c <= hold) cl[ctas] = c;
+    }
+    const int ctas = cl[2] == 0 || cl[2] >= 4 * cl[1] ? 1 : 2;
+    // A list of 1 / 8 of a slice's vectors or more takes the list warps longer than the slice takes the
+    // others; the kernels below work through it with all of theirs (1024 rows, ring and below: 32000
+    // wide, k = 400 74 and 64, 512 82 and 66, 1024 137 and 76; 50001 wide, 512 86 and 109, 700 111 and
+    // 117, 1024 139 and 129; 300000 wide, 512 492 and 559, 700 795 and 543; 128256 wide, 700 217 and 270,
+    // 1024 266 and 293).
+    if (vecs > DS_RING_MIN_VECS && cl[ctas] > 0 && 8 * a.k < (vecs + cl[ctas] - 1) / cl[ctas] &&
+        static_cast<int64_t>(n) * cl[ctas] >= 2 * ctas * device_sms()) {
+      a.cl = cl[ctas];
       a.per = cut();
-      if (a.per <= hold * DS_CHUNK_VECS &&
-          static_cast<int64_t>(n) * a.cl >= 2 * ctas * device_sms())
-        return launch_ring<T, D>(a, n, ctas, stream);
+      return launch_ring<T, D>(a, n, ctas, stream);
     }
   }
   // Slices: enough to give every SM two CTAs when rows are few, none shorter than one vector per
