@@ -3,7 +3,7 @@
 //
 //   quant_*_kernel        x' = V S_X^-1 x, a = max |x'| per token, s = a / 127,
 //                         q = rint(x' / s) (of the exact quotient, ties to even), sum = sum q
-//   out_transform_kernel  y = S_G^-1 U^T y' (signs after the Hadamard blocks, which are symmetric)
+//   out_*_kernel          y = S_G^-1 U^T y' (signs after the Hadamard blocks, which are symmetric)
 //
 // Hadamard stages commute, so each of them runs where its elements share a thread. A row takes three
 // phases, with the row in shared memory between them:
@@ -13,7 +13,7 @@
 //   strips   of 32 neighbours (bits 2 .. 4, or 0 .. 4)
 // Groups touch device memory in whole lines, with the channel scales and signs they need, columns do
 // for fp32. The token pass ends with the strips, which stay in registers until the token's scale is
-// known; the output pass takes columns, strips, groups.
+// known; the output pass takes columns, strips, groups (short blocks have a kernel of their own).
 #include <cuda_bf16.h>
 
 #include <algorithm>
