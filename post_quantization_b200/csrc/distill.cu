@@ -1239,8 +1239,8 @@ kronq_status launch_distill(DsArgs a, int n, bool lse, bool grad, cudaStream_t s
     // Long rows, at least two per cluster: the fewest CTAs that hold a row with two chunks to spare.
     // Two CTAs per SM, unless the list takes so much of their memory that a row needs four times the
     // CTAs, each of which works through the list (1024 rows, us with two and with one: 128256 wide,
-    // k = 128 (4 and 2 CTAs) 128 and 154, k = 256 (8 and 2) 208 and 158, k = 512 301 and 184; 50001
-    // wide, k = 256 (4 and 1) 99 and 78; 32000 wide, k = 256 (2 and 1) 56 and 60).
+    // k = 256 (8 and 2 CTAs) 254 and 158, k = 512 408 and 203; 50001 wide, k = 256 (4 and 1) 127 and 78;
+    // 128256 wide, k = 128 (4 and 2) 128 and 154).
     int cl[3] = {0, 0, 0};                       // by CTAs per SM; 0: a row does not fit
     for (int ctas = 1; ctas <= 2; ++ctas) {
       const int64_t hold = static_cast<int64_t>(ring_chunks(a, ctas) - 2) * DS_CHUNK_VECS;
@@ -1249,10 +1249,9 @@ kronq_status launch_distill(DsArgs a, int n, bool lse, bool grad, cudaStream_t s
     }
     const int ctas = cl[2] == 0 || cl[2] >= 4 * cl[1] ? 1 : 2;
     // A list of 1 / 8 of a slice's vectors or more takes the list warps longer than the slice takes the
-    // others; the kernels below work through it with all of theirs (1024 rows, ring and below: 32000
-    // wide, k = 400 74 and 64, 512 82 and 66, 1024 137 and 76; 50001 wide, 512 86 and 109, 700 111 and
-    // 117, 1024 139 and 129; 300000 wide, 512 492 and 559, 700 795 and 543; 128256 wide, 700 217 and 270,
-    // 1024 266 and 293).
+    // others; the kernels below work through it with all of theirs (1024 rows, us, ring and below: 32000
+    // wide, k = 300 74 and 66, 512 111 and 72; 50001 wide, 512 117 and 125, 700 137 and 131, 1024 195 and
+    // 158; 128256 wide, 700 246 and 295, 1024 348 and 340; 300000 wide, 512 453 and 547, 700 990 and 567).
     if (vecs > DS_RING_MIN_VECS && cl[ctas] > 0 && 8 * a.k < (vecs + cl[ctas] - 1) / cl[ctas] &&
         static_cast<int64_t>(n) * cl[ctas] >= 2 * ctas * device_sms()) {
       a.cl = cl[ctas];
