@@ -663,6 +663,10 @@ __device__ __forceinline__ float ds_coef(float wt, float mass, float s) {
 // before the CTA's first warp sends: no CTA stores a part of the row (dz may be z) before every
 // z[id] of it is read. It stores the listed entries' gradients when the warps have stored the row's
 // (barrier stored).
+//
+// 4096 x 128256 bf16, k = 128: 475 us, 4.4 TB/s read and written (floor 325 us; the two exponentials an
+// element take 233 of their unit). Reading the row again from L2 instead of the ring took 592 us, three
+// CTAs per SM with shorter rings 619.
 template <typename T, typename D>
 __global__ void __launch_bounds__(DS_RING_THREADS, 2)
     distill_ring_kernel(DsArgs a, int64_t n, int chunks, int* err) {
@@ -1001,7 +1005,8 @@ __global__ void __launch_bounds__(DS_RING_THREADS, 2)
   }
 }
 
-// Loss and gradient; NV vectors of z per thread stay in registers.
+// Loss and gradient; NV vectors of z per thread stay in registers. 96 x 50001 bf16: 9.3 us of the GPU,
+// the launch, one read and the barriers' latency; 256 x 128256: 44 us, 3 TB/s.
 template <typename T, typename D, int NV, int KPT>
 __global__ void __launch_bounds__(DS_THREADS, NV > 8 ? 2 : (KPT == 1 ? 4 : 3)) distill_hold_kernel(DsArgs a) {
   __shared__ DsShared sh;
@@ -1069,7 +1074,9 @@ __global__ void __launch_bounds__(DS_THREADS, NV > 8 ? 2 : (KPT == 1 ? 4 : 3)) d
   if (a.cl > 1) ds_cluster_wait();                     // a peer may still read this CTA's sums
 }
 
-// LSE: the row's statistics are taken from z (else lse_in). GRAD: dz is written.
+// LSE: the row's statistics are taken from z (else lse_in). GRAD: dz is written. Bound by HBM on long
+// rows: the loss of 4096 x 128256 bf16 at 6.4 TB/s (163 us), the gradient from lse of 1024 x 32000 fp32
+// at 5.2 TB/s (50 us).
 template <typename T, typename D, bool LSE, bool GRAD, int KPT>
 __global__ void __launch_bounds__(DS_THREADS) distill_stream_kernel(DsArgs a) {
   __shared__ DsShared sh;
