@@ -955,9 +955,9 @@ __global__ void __launch_bounds__(DS_RING_THREADS, 2)
         }
       }
       if (s.edge >= 0 && ze != kNegInf) {
+        // the maximum's own term too: 2^(ze c - fl(ze c)) is not 1, and +inf makes it NaN
         const float m = fmaxf(rs.m, ze);
-        rs.s = (rs.m == m ? rs.s : rs.s * ds_rescale(rs.m, m, a.c)) +
-               (ze == m ? 1.f : ex2(ds_exponent(ze, m, a.c)));         // NaN stays NaN
+        rs.s = (rs.m == m ? rs.s : rs.s * ds_rescale(rs.m, m, a.c)) + ex2(ds_exponent(ze, m, a.c));
         rs.m = m;
       }
       rs = ds_join_lanes<32>(rs, a.c);

@@ -1,0 +1,117 @@
+"""Distillation on long rows: many of them (clusters that take rows in turn, at 1, 2, 4 and 8 CTAs a
+row), and few (rows read twice), vs the definition in fp64 on the device.
+
+Bounds: a thread adds at most V / 256 + 64 terms and joins of relative error 2^-23 each, so sums, and
+with them q, are off by STAT = (V / 256 + 64) 2^-23 relative. An exponent is one FMA against a rounded
+reference; the reference's rounding is the same number in the sum and in q, so only the exponent's own
+rounding is left, 2^-24 of its size, whatever z / tau is.
+"""
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+U32 = 2.0 ** -24
+HALF = {torch.float32: U32, torch.bfloat16: 2.0 ** -8}
+BF16, F32 = torch.bfloat16, torch.float32
+
+# rows, vocabulary, type: 1, 2, 4 and 8 CTAs a row by the rule of distill.cu; every vocabulary is odd, so
+# that rows begin and end beside their 16-byte vectors
+RING = [(600, 20011, BF16), (300, 50257, BF16), (150, 128257, BF16), (80, 240001, BF16),
+        (300, 20011, F32)]
+# few rows, which registers hold, and too long for that
+FEW = [(5, 20011, BF16), (5, 20011, F32), (3, 300001, BF16), (3, 140001, F32)]
+
+
+@pytest.fixture(scope="module")
+def K():
+    from post_quantization_b200 import build
+    build.build()
+    from post_quantization_b200 import kronq
+    kronq.load_library()
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    kronq.kronq_device_check()
+    return kronq
+
+
+def inputs(n, v, k, dtype, seed):
+    """Student logits near a teacher's list of distinct entries (in fp32)."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    z = torch.empty(n, v, dtype=dtype, device="cuda")
+    for r in range(0, n, 100):
+        z[r:r + 100] = 2.0 * torch.randn(min(100, n - r), v, generator=g, device="cuda")
+    start = torch.randint(0, v, (n, 1), generator=g, device="cuda")
+    step = torch.randint(1, v // k, (n, 1), generator=g, device="cuda")
+    ids = (start + torch.arange(k, device="cuda") * step) % v
+    t = 9.0 - 4.0 * torch.rand(n, k, generator=g, device="cuda")
+    z.scatter_(1, ids, (t + 0.5 * torch.randn(n, k, generator=g, device="cuda")).to(dtype))
+    return z, ids.to(torch.int32), t
+
+
+def run(K, z, ids, t, tau=1.0, w=None, dz=None):
+    loss = torch.full((z.shape[0],), 7.0, device="cuda")
+    lse = torch.full((z.shape[0],), 7.0, device="cuda")
+    if dz is None:
+        dz = torch.full(z.shape, 7.0, dtype=z.dtype, device="cuda")
+    K.kronq_distill(z, ids, t, loss, lse, dlogits=dz, row_weight=w, temperature=tau)
+    torch.cuda.synchronize()
+    return loss, lse, dz
+
+
+def exact(z, ids, t, tau, w=None):
+    """(loss, lse, q, gradient) of rows with finite logits at their listed entries."""
+    u = z.double() / tau
+    lse = torch.logsumexp(u, 1)
+    there = ids >= 0
+    at = ids.clamp(min=0).long()
+    logp = torch.log_softmax((t.double() / tau).masked_fill(~there, -math.inf), 1)
+    logp = logp.masked_fill(~there, -math.inf)         # a row without entries too
+    p = logp.exp()
+    w = torch.ones(z.shape[0], dtype=torch.float64, device="cuda") if w is None else w.double()
+    terms = p * (logp - u.gather(1, at) + lse[:, None])
+    loss = w * tau * tau * terms.masked_fill(p == 0, 0.0).sum(1)
+    q = (u - lse[:, None]).exp()
+    unit = (w * tau)[:, None]
+    grad = unit * (q * p.sum(1, keepdim=True) - torch.zeros_like(q).scatter_add_(1, at, p))
+    return loss, lse, q, grad
+
+
+@pytest.mark.parametrize("n,v,dtype", RING + FEW)
+@pytest.mark.parametrize("bad", [math.inf, math.nan])
+def test_logits_that_are_not_finite(K, n, v, dtype, bad):
+    """+inf or NaN anywhere in a row (its first and last elements lie beside the vectors) makes the row
+    NaN, and no other."""
+    k = 20
+    z, ids, t = inputs(n, v, k, dtype, v)
+    ok = run(K, z, ids, t)
+    rows = list(range(0, n, max(1, n // 40)))
+    for i, r in enumerate(rows):
+        z[r, (0, v - 1, v // 2, 1, v - 2, int(ids[r, 3]))[i % 6]] = bad
+    loss, lse, dz = run(K, z, ids, t)
+    hit = torch.zeros(n, dtype=torch.bool, device="cuda")
+    hit[rows] = True
+    assert bool(loss[hit].isnan().all()) and bool(lse[hit].isnan().all())
+    assert bool(dz[hit].isnan().all())
+    assert torch.equal(loss[~hit], ok[0][~hit]) and torch.equal(lse[~hit], ok[1][~hit])
+    assert torch.equal(dz[~hit], ok[2][~hit])
+    assert K.kronq_device_error() == 0
+
+
+@pytest.mark.parametrize("n,v,dtype", [c for c in RING + FEW if c[2] == F32])
+@pytest.mark.parametrize("side", [0, -1])
+def test_maximum_beside_the_vectors_at_a_small_temperature(K, n, v, dtype, side):
+    """A row's first or last element far above the others: q there is 1 however large z / tau is."""
+    tau = 2.0 ** -8
+    z, ids, t = inputs(n, v, 4, dtype, v + 1)
+    z.clamp_(max=20.0)
+    z[:, side] = 90.0 + torch.rand(n, device="cuda")   # z / tau near 23000
+    ids[:, 0] = v // 2
+    ids[:, 1:] = -1                                    # p = 1 in the middle
+    loss, lse, dz = run(K, z, ids, t, tau)
+    _, _, q, grad = exact(z, ids, t, tau)
+    stat = (v / 256 + 64) * 2.0 ** -23
+    tol = (stat + U32) * tau
+    assert float((dz[:, side].double() - grad[:, side]).abs().max()) <= tol
