@@ -251,8 +251,10 @@ __device__ __forceinline__ bool ds_wide(float m, float c) { return !(fabsf(m * c
 __device__ __forceinline__ float ds_exponent(float z, float m, float c) {
   return ds_wide(m, c) ? (z - m) * c : fmaf(z, c, -(m * c));
 }
+// From a sum's reference to another. Both products are rounded as in ds_exponent: a contraction into one
+// FMA would leave that of `from` exact, and the sums off by its rounding (at tau = 2^-8 by 1e-3).
 __device__ __forceinline__ float ds_rescale(float from, float to, float c) {
-  return ex2(ds_wide(to, c) ? (from - to) * c : from * c - to * c);
+  return ex2(ds_wide(to, c) ? (from - to) * c : __fsub_rn(__fmul_rn(from, c), __fmul_rn(to, c)));
 }
 // Joins groups of W consecutive lanes that hold the same W values in every group (W = 32: the
 // warp): the common maximum first, so that each lane rescales its sum once.

@@ -115,3 +115,35 @@ def test_maximum_beside_the_vectors_at_a_small_temperature(K, n, v, dtype, side)
     stat = (v / 256 + 64) * 2.0 ** -23
     tol = (stat + U32) * tau
     assert float((dz[:, side].double() - grad[:, side]).abs().max()) <= tol
+
+
+@pytest.mark.parametrize("n,v,dtype", [c for c in RING + FEW if c[2] == F32])
+def test_close_logits_at_a_small_temperature(K, n, v, dtype):
+    """A dozen entries within a few tau of the maximum, in different threads, z / tau near 23000: each
+    thread's reference rounds by up to 2^-10, which has to cancel where the sums are joined.
+
+    Tolerance: q and p are each off by STAT and 8 2^-23 (an exponent below 8 rounded by 2^-24 of its
+    size, the exponential's two steps, p's rounding), the mass P by the same; a loss term log p - log q
+    is below 10."""
+    k, tau, top = 8, 2.0 ** -8, 12
+    g = torch.Generator(device="cuda")
+    g.manual_seed(v)
+    z, _, _ = inputs(n, v, k, dtype, v + 2)
+    z.clamp_(max=20.0)
+    start = torch.randint(0, v, (n, 1), generator=g, device="cuda")
+    at = (start + torch.arange(top, device="cuda") * (v // top - 1)) % v
+    z.scatter_(1, at, 90.0 - 3 * tau * torch.rand(n, top, generator=g, device="cuda"))
+    ids = at[:, :k].to(torch.int32)
+    t = 90.0 - 3 * tau * torch.rand(n, k, generator=g, device="cuda")
+    loss, lse, dz = run(K, z, ids, t, tau)
+    alone = torch.empty(n, device="cuda")
+    K.kronq_distill(z, ids, t, alone, temperature=tau)
+    torch.cuda.synchronize()
+    wl, wlse, q, wg = exact(z, ids, t, tau)
+    rel = (v / 256 + 64) * 2.0 ** -23 + 8 * 2.0 ** -23
+    p = torch.softmax(t.double() / tau, 1)
+    size = tau * (2 * q + torch.zeros_like(q).scatter_add_(1, at[:, :k], p))
+    assert bool(((dz.double() - wg).abs() <= rel * size + U32 * wg.abs() + 1e-38).all())
+    assert bool(((lse.double() - wlse).abs() <= rel + U32 * wlse.abs()).all())
+    for got in (loss, alone):
+        assert bool(((got.double() - wl).abs() <= tau * tau * 12 * rel + U32 * wl.abs()).all())
