@@ -678,8 +678,8 @@ kronq_status kronq_qlinear8(const void* x, int32_t x_dtype, int64_t ld_x, int32_
   if ((flags & KRONQ_BIIP_SCALE_OUT) && !s_g) return fail(KRONQ_ERR_INVALID_ARG, "s_g is NULL");
   const bool rot_out = (flags & KRONQ_BIIP_ROTATE_OUT) != 0;
   if (rot_out && !sign_out) return fail(KRONQ_ERR_INVALID_ARG, "sign_out is NULL");
-  if (rot_out && (d_out & -d_out) > 16384)
-    return fail(KRONQ_ERR_UNSUPPORTED, "Hadamard blocks above 16384 are not supported");
+  if (rot_out && (d_out & -d_out) > kMaxOutBlock)
+    return fail(KRONQ_ERR_UNSUPPORTED, "Hadamard blocks above %d are not supported", kMaxOutBlock);
   KQ_TRY(check_float_matrix(y, y_dtype, ld_y, n_tok, d_out, "y"));
   const Qlinear8Plan plan = qlinear8_plan(n_tok, d_out, d_in, flags);
   KQ_TRY(check_ws(workspace, workspace_bytes, plan.total()));

@@ -1192,8 +1192,9 @@ kronq_status launch_rows(void (*kern)(DsArgs), DsArgs a, int n, bool cluster, bo
 size_t ring_list_bytes(const DsArgs& a) {
   return 8 * (static_cast<size_t>(id_table_words(a)) + 4 * a.k);
 }
+int ring_room(int ctas) { return (ctas == 2 ? 111 : 224) * 1024; }     // per CTA
 int ring_chunks(const DsArgs& a, int ctas) {
-  const int64_t room = (ctas == 2 ? 111 : 224) * 1024 - static_cast<int64_t>(ring_list_bytes(a));
+  const int64_t room = ring_room(ctas) - static_cast<int64_t>(ring_list_bytes(a));
   return static_cast<int>(std::min<int64_t>(DS_MAX_CHUNKS, room / (DS_CHUNK_VECS * 16)));
 }
 
@@ -1202,8 +1203,9 @@ kronq_status launch_ring(const DsArgs& a, int n, int ctas, cudaStream_t stream) 
   const int chunks = ring_chunks(a, ctas);
   const size_t smem = static_cast<size_t>(chunks) * DS_CHUNK_VECS * 16 + ring_list_bytes(a);
   auto kern = distill_ring_kernel<T, D>;
-  KQ_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   static_cast<int>(smem)));
+  // the most of any call: calls of other threads launch this kernel with other lists
+  static std::atomic<uint64_t> allowed{0};
+  KQ_TRY(allow_smem(reinterpret_cast<const void*>(kern), ring_room(1), allowed));
   int* err = device_error_word();
   if (!err) return fail(KRONQ_ERR_CUDA, "device error word unavailable");
   // As many clusters as run at once: one more would start when all others have ended. The query

@@ -138,6 +138,7 @@ struct QuantTokensArgs {
   int chained;             // launched in front of the layer's product
 };
 constexpr int kMaxRotatedWidth = 53248;  // a rotated token is held in shared memory (fp32)
+constexpr int kMaxOutBlock = 16384;      // and a Hadamard block of the output
 kronq_status run_quant_tokens(const QuantTokensArgs& q, cudaStream_t stream);
 // y = S_G^-1 U^T yp for n <= 65535 tokens (s_g NULL: no scaling)
 kronq_status run_out_transform(const float* yp, int64_t ld_yp, int n, int d, const float* s_g,

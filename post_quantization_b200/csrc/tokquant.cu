@@ -910,6 +910,19 @@ int log2_of(int b) {
 }
 size_t row_smem(int len) { return static_cast<size_t>((len + 31) / 32) * 32 * sizeof(float); }
 
+// A kernel as a type, so that what is kept for a kernel has a place of its own.
+template <auto K>
+struct Kern {
+  static constexpr auto value = K;
+};
+// Lets a kernel hold the longest row that it is ever launched with: the limit belongs to the kernel, not
+// to the call, and calls of other threads launch it with rows of other lengths.
+template <auto K>
+kronq_status allow_row(int longest) {
+  static std::atomic<uint64_t> allowed{0};
+  return allow_smem(reinterpret_cast<const void*>(K), row_smem(longest), allowed);
+}
+
 }  // namespace
 
 kronq_status run_quant_tokens(const QuantTokensArgs& q, cudaStream_t stream) {
@@ -935,22 +948,22 @@ kronq_status run_quant_tokens(const QuantTokensArgs& q, cudaStream_t stream) {
   // unrotated: two units a thread as far as TQ_THREADS go
   const int threads = smem_row ? row_threads(q.d)
                                : std::min(TQ_THREADS, std::max(32, ((units + 1) / 2 + 31) / 32 * 32));
-  auto launch = [&](auto kern) -> kronq_status {
-    if (smem > 48 * 1024)
-      KQ_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem)));
-    return launch_chained(kern, dim3(q.n), dim3(threads), smem, stream, 1, "quantize_tokens kernel", a);
+  auto run = [&](auto kern) -> kronq_status {
+    if (smem_row) KQ_TRY(allow_row<decltype(kern)::value>(kMaxRotatedWidth));
+    return launch_chained(decltype(kern)::value, dim3(q.n), dim3(threads), smem, stream, 1,
+                          "quantize_tokens kernel", a);
   };
+  auto launch = [&](auto aligned, auto other) { return vec ? run(aligned) : run(other); };
   auto typed = [&](auto x) -> kronq_status {
     using T = decltype(x);
     if (smem_row)
       switch (top_bits(a.log_b)) {
-        case 0: return vec ? launch(quant_rotated_kernel<T, true, 0>) : launch(quant_rotated_kernel<T, false, 0>);
-        case 1: return vec ? launch(quant_rotated_kernel<T, true, 1>) : launch(quant_rotated_kernel<T, false, 1>);
-        case 2: return vec ? launch(quant_rotated_kernel<T, true, 2>) : launch(quant_rotated_kernel<T, false, 2>);
-        default: return vec ? launch(quant_rotated_kernel<T, true, 3>) : launch(quant_rotated_kernel<T, false, 3>);
+        case 0: return launch(Kern<quant_rotated_kernel<T, true, 0>>(), Kern<quant_rotated_kernel<T, false, 0>>());
+        case 1: return launch(Kern<quant_rotated_kernel<T, true, 1>>(), Kern<quant_rotated_kernel<T, false, 1>>());
+        case 2: return launch(Kern<quant_rotated_kernel<T, true, 2>>(), Kern<quant_rotated_kernel<T, false, 2>>());
+        default: return launch(Kern<quant_rotated_kernel<T, true, 3>>(), Kern<quant_rotated_kernel<T, false, 3>>());
       }
-    return vec ? launch(quant_plain_kernel<T, true>) : launch(quant_plain_kernel<T, false>);
+    return launch(Kern<quant_plain_kernel<T, true>>(), Kern<quant_plain_kernel<T, false>>());
   };
   return q.x_dtype == KRONQ_DTYPE_BF16 ? typed(__nv_bfloat16()) : typed(0.f);
 }
@@ -980,19 +993,19 @@ kronq_status run_out_transform(const float* yp, int64_t ld_yp, int n, int d, con
   const bool units = a.b <= 1024;
   const int threads = units ? unit_threads(a.span / 8) : row_threads(a.span);
   const size_t smem = a.b <= 8 ? 0 : units ? unit_smem(a.span) : row_smem(a.span);
-  auto launch = [&](auto kern) -> kronq_status {
-    if (smem > 48 * 1024)
-      KQ_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem)));
-    return launch_chained(kern, grid, dim3(threads), smem, stream, 1, "output transform kernel", a);
+  auto run = [&](auto kern) -> kronq_status {
+    if (!units) KQ_TRY(allow_row<decltype(kern)::value>(kMaxOutBlock));
+    return launch_chained(decltype(kern)::value, grid, dim3(threads), smem, stream, 1,
+                          "output transform kernel", a);
   };
+  auto launch = [&](auto aligned, auto other) { return vec ? run(aligned) : run(other); };
   auto typed = [&](auto out) -> kronq_status {
     using Y = decltype(out);
-    if (units) return vec ? launch(out_units_kernel<Y, true>) : launch(out_units_kernel<Y, false>);
+    if (units) return launch(Kern<out_units_kernel<Y, true>>(), Kern<out_units_kernel<Y, false>>());
     switch (top_bits(a.log_b)) {
-      case 1: return vec ? launch(out_transform_kernel<Y, true, 1>) : launch(out_transform_kernel<Y, false, 1>);
-      case 2: return vec ? launch(out_transform_kernel<Y, true, 2>) : launch(out_transform_kernel<Y, false, 2>);
-      default: return vec ? launch(out_transform_kernel<Y, true, 3>) : launch(out_transform_kernel<Y, false, 3>);
+      case 1: return launch(Kern<out_transform_kernel<Y, true, 1>>(), Kern<out_transform_kernel<Y, false, 1>>());
+      case 2: return launch(Kern<out_transform_kernel<Y, true, 2>>(), Kern<out_transform_kernel<Y, false, 2>>());
+      default: return launch(Kern<out_transform_kernel<Y, true, 3>>(), Kern<out_transform_kernel<Y, false, 3>>());
     }
   };
   return y_dtype == KRONQ_DTYPE_BF16 ? typed(__nv_bfloat16()) : typed(0.f);
