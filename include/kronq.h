@@ -418,7 +418,8 @@ KRONQ_API kronq_status kronq_qlinear(const void* x, int32_t x_dtype, int64_t ld_
  *            pointer may be NULL. d_in <= 65536, with ROTATE_IN <= 53248 (KRONQ_ERR_UNSUPPORTED)
  *   q        (device, int8) n_tok x d_in, row stride ld_q bytes; bytes past d_in stay as they are
  *   tok_scale (device, fp32), tok_sum (device, int32): n_tok each
- *   Arithmetic: x' in fp32; s_t = max|x'| / 127 rounded once; q is the exact quotient x' / s_t
+ *   Arithmetic: x' in fp32 (x / s_x rounded once, with Hadamard blocks above 8 to 2 ulp; subnormal
+ *   numbers count); s_t = max|x'| / 127 rounded once; q is the exact quotient x' / s_t
  *   rounded to the nearest integer, ties to even, so |q| <= 127. A token whose s_t would be below
  *   2^-126 (all zero, say) has q = 0, s_t = 1. A token with an infinity or a NaN in x' (with
  *   ROTATE_IN also in a sum of a Hadamard block, sqrt(block) x') has q = 0 and s_t = NaN, which
@@ -453,8 +454,10 @@ KRONQ_API kronq_status kronq_matmul_i8(const int8_t* q, int64_t ld_q, const floa
 /* kronq_qlinear8 - y = S_G^-1 U^T W^' V S_X^-1 x in 8-bit integers, for any number of tokens.
  *
  *   The arguments of the two calls above; s_x, s_g, sign_in, sign_out, flags as for kronq_qlinear
- *   (Hadamard blocks of the output up to 16384). The transforms are applied in fp32, y is rounded
- *   once. workspace: kronq_qlinear8_workspace_size(n_tok, d_out, d_in, flags) bytes; it does not
+ *   (Hadamard blocks of the output up to 16384). The transforms are applied in fp32: with
+ *   ROTATE_OUT each stage and the product with 1 / sqrt(block) round once and the quotient by s_g is
+ *   good to 2 ulp, without it s_o / s_g takes the place of s_o. The result is rounded to y's type.
+ *   workspace: kronq_qlinear8_workspace_size(n_tok, d_out, d_in, flags) bytes; it does not
  *   grow past 16384 tokens (2048 with ROTATE_OUT), which are then taken in turn. */
 KRONQ_API size_t kronq_qlinear8_workspace_size(int32_t n_tok, int32_t d_out, int32_t d_in,
                                                uint32_t flags);
