@@ -829,6 +829,7 @@ __global__ void __launch_bounds__(DS_RING_THREADS, 2)
       }
 #pragma unroll
       for (int o = 16; o; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
+      __syncwarp();              // every lane has its z[id]: from here on the row may be overwritten
       if (lane == 0) {
         masses[turn] = mass;
         mbar_arrive(&ready[turn]);
@@ -852,6 +853,7 @@ __global__ void __launch_bounds__(DS_RING_THREADS, 2)
           if (old[b] != -1) again |= table.settle(a, j0 + 32 * b, h[b], old[b]);
       }
       again = __any_sync(0xffffffffu, again);
+      __syncwarp();              // the table's other lanes' entries: a vote alone orders no memory
       if (again) {
         for (int j = lane; j - lane < a.k; j += 32) {
           bool mine = j < a.k && own[j] >= 0;
