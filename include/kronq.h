@@ -497,8 +497,11 @@ KRONQ_API kronq_status kronq_qlinear8(const void* x, int32_t x_dtype, int64_t ld
  *   dlogits  (device) n_tok x vocab, dlogits_dtype BF16 or F32, row stride ld_dlogits, or NULL (the
  *            loss alone). It may be logits itself (same type and stride), not overlap it otherwise
  *   n_tok = 0 is a no-op. Sums and softmax statistics in fp32 or fp64. Deterministic.
+ *   A row of one large finite value (a mask of -1e30, say) is a uniform row: q = 1 / vocab
  * kronq_distill_backward gives the gradient alone, from lse (as kronq_distill returned it) and the
- * upstream gradient dloss (device, fp32, n_tok), which takes the place of w.
+ * upstream gradient dloss (device, fp32, n_tok), which takes the place of w. lse comes rounded to
+ * fp32, so q is off by the factor exp(2^-24 |lse|) at most; where |lse| passes 2^24 (a row of nothing
+ * but masks) that says nothing about q, and only kronq_distill's own gradient does.
  * ------------------------------------------------------------------------------------- */
 KRONQ_API kronq_status kronq_distill(const void* logits, int32_t logits_dtype, int64_t ld_logits,
                                      const int32_t* ids, int64_t ld_ids, const void* top,

@@ -8,8 +8,8 @@
 // z is streamed with a running maximum m and sum per thread: sum of 2^(z c - fl(m c)), with
 // c = log2(e) / tau. The exponent is one FMA, rounded relative to the small difference; the
 // rounding of m c is the same in a row's sum and in its q, where it cancels, and lse undoes it.
-// Where m c overflows (a row that holds nothing but the type's lowest value) the exponent is
-// (z - m) c instead.
+// Where |m c| is 2^20 or more (a row that holds nothing but a mask's large value, say) the exponent
+// is (z - m) c instead: there the rounding of m c could leave the range of 2^x.
 // Per element: an unpack, half a packed fp32 FMA, one ex2 (16 a cycle and SM), half a packed add.
 //
 // A row is cut into cl slices of 16-byte vectors, one CTA each. Where the row's statistics are
@@ -246,15 +246,19 @@ __device__ __forceinline__ bool store_aligned(const Slice<T>& s, const D* dz) {
 struct __align__(8) RunSum {      // sent as one 8-byte word
   float m, s;
 };
-__device__ __forceinline__ bool ds_wide(float m, float c) { return !(fabsf(m * c) < INFINITY); }
+__device__ __forceinline__ bool ds_wide(float m, float c) { return !(fabsf(m * c) < 1048576.f); }
 // the exponent of one element
 __device__ __forceinline__ float ds_exponent(float z, float m, float c) {
   return ds_wide(m, c) ? (z - m) * c : fmaf(z, c, -(m * c));
 }
-// From a sum's reference to another. Both products are rounded as in ds_exponent: a contraction into one
-// FMA would leave that of `from` exact, and the sums off by its rounding (at tau = 2^-8 by 1e-3).
+// From a sum's reference to another. Narrow references are rounded products, as in ds_exponent: a
+// contraction into one FMA would leave that of `from` exact, and the sums off by its rounding (at
+// tau = 2^-8 by 1e-3). Of a narrow and a wide one the wide one's product is exact.
 __device__ __forceinline__ float ds_rescale(float from, float to, float c) {
-  return ex2(ds_wide(to, c) ? (from - to) * c : __fsub_rn(__fmul_rn(from, c), __fmul_rn(to, c)));
+  const bool wide_from = ds_wide(from, c), wide_to = ds_wide(to, c);
+  const float f = __fmul_rn(from, c), t = __fmul_rn(to, c);
+  if (wide_from != wide_to) return ex2(wide_to ? -fmaf(to, c, -f) : fmaf(from, c, -t));
+  return ex2(wide_to ? (from - to) * c : __fsub_rn(f, t));
 }
 // Joins groups of W consecutive lanes that hold the same W values in every group (W = 32: the
 // warp): the common maximum first, so that each lane rescales its sum once.
@@ -446,9 +450,19 @@ __device__ __forceinline__ void gather_logits(const Slice<T>& s, int part, bool 
   }
 }
 
-// -inf where nothing was seen
-__device__ __forceinline__ double ds_lse(const DsArgs& a, RunSum r) {
-  return (ds_wide(r.m, a.c) ? r.m * a.inv_tau : r.m * a.c * a.nat) + logf(r.s);
+// A log-sum in two parts, the reference's and the sum's: a logit's distance from it keeps the second
+// where the first is large. -inf where nothing was seen.
+struct LogSum {
+  double ref;
+  float log;
+  __device__ __forceinline__ double total() const { return ref + log; }
+};
+__device__ __forceinline__ LogSum ds_lse(const DsArgs& a, RunSum r) {
+  return {ds_wide(r.m, a.c) ? __dmul_rn(r.m, a.inv_tau) : r.m * a.c * a.nat, logf(r.s)};
+}
+// log of an entry's share. The product is rounded as that of the reference: equal ones cancel.
+__device__ __forceinline__ double ds_log_share(const DsArgs& a, float x, LogSum l) {
+  return __dsub_rn(__dmul_rn(x, a.inv_tau), l.ref) - l.log;
 }
 
 // Joins the CTA's statistics, the row's (exchange: what other CTAs have) and the listed entries';
@@ -497,27 +511,27 @@ __device__ __forceinline__ void row_statistics(const DsArgs& a, int64_t row, int
     if (a.cl > 1) rs = exchange(rs);
   }
   double part_loss = 0.0;
-  const double lse = report ? ds_lse(a, rs) : 0.0;
+  const LogSum lse = report ? ds_lse(a, rs) : LogSum{0.0, 0.f};
   mass = 0.f;
 #pragma unroll
   for (int i = 0; i < KPT; ++i) e.p[i] = 0.f;
   if (lists) {
     // log p_j = t_j / tau - L_t in fp64: the difference of two numbers of the logits' size
     ls = ds_join_lanes<NW>(sh.list[lane % NW], a.c);
-    const double norm = a.top_lse ? static_cast<double>(top_lse) : ds_lse(a, ls);
+    const LogSum norm = a.top_lse ? LogSum{static_cast<double>(top_lse), 0.f} : ds_lse(a, ls);
 #pragma unroll
     for (int i = 0; i < KPT; ++i) {
       const int j = tid + i * NT;
       if (j >= a.k) break;
       if (e.t[i] != kNegInf) {
-        const double lp = e.t[i] * a.inv_tau - norm;
+        const double lp = ds_log_share(a, e.t[i], norm);
         const float p = expf(static_cast<float>(lp));
         e.p[i] = p;
         mass += p;
         // a listed entry that the student masks has an infinite loss
         if (report && p != 0.f)
           part_loss += e.z[i] == kNegInf ? static_cast<double>(INFINITY)
-                                         : p * (lp - e.z[i] * a.inv_tau + lse);
+                                         : p * (lp - ds_log_share(a, e.z[i], lse));
       }
       if (GRAD) {
         const IdTable table(a, table_mem);
@@ -548,7 +562,7 @@ __device__ __forceinline__ void row_statistics(const DsArgs& a, int64_t row, int
     double tot = 0.0;
     for (int i = 0; i < NW; ++i) tot += sh.loss[i];
     a.loss[row] = w == 0.f ? 0.f : static_cast<float>(static_cast<double>(w) * a.tau * a.tau * tot);
-    if (a.lse) a.lse[row] = static_cast<float>(lse);
+    if (a.lse) a.lse[row] = static_cast<float>(lse.total());
   }
 }
 
@@ -812,7 +826,8 @@ __global__ void __launch_bounds__(DS_RING_THREADS, 2)
       }
       ls = ds_join_lanes<32>(ls, a.c);
       // log p_j = t_j / tau - L_t in fp64: the difference of two numbers of the logits' size
-      const double norm = a.top_lse ? static_cast<double>(a.top_lse[row]) : ds_lse(a, ls);
+      const LogSum norm =
+          a.top_lse ? LogSum{static_cast<double>(a.top_lse[row]), 0.f} : ds_lse(a, ls);
       float mass = 0.f;
       for (int j0 = lane; j0 < a.k; j0 += 32 * B) {
         float p[B];
@@ -820,7 +835,7 @@ __global__ void __launch_bounds__(DS_RING_THREADS, 2)
         for (int b = 0; b < B; ++b) p[b] = j0 + 32 * b < a.k ? t[j0 + 32 * b] : kNegInf;
 #pragma unroll
         for (int b = 0; b < B; ++b) {
-          p[b] = p[b] == kNegInf ? 0.f : expf(static_cast<float>(p[b] * a.inv_tau - norm));
+          p[b] = p[b] == kNegInf ? 0.f : expf(static_cast<float>(ds_log_share(a, p[b], norm)));
           mass += p[b];
         }
 #pragma unroll
@@ -886,7 +901,7 @@ __global__ void __launch_bounds__(DS_RING_THREADS, 2)
         }
       }
       if (part == 0) {
-        const double lse = ds_lse(a, rs);
+        const LogSum lse = ds_lse(a, rs);
         double loss = 0.0;
         for (int j0 = lane; j0 < a.k; j0 += 32 * B) {
           float p[B], x[B], z[B];
@@ -901,14 +916,15 @@ __global__ void __launch_bounds__(DS_RING_THREADS, 2)
           for (int b = 0; b < B; ++b)
             if (p[b] != 0.f)                          // a masked listed entry: infinite loss
               loss += z[b] == kNegInf ? static_cast<double>(INFINITY)
-                                      : p[b] * ((static_cast<double>(x[b]) - z[b]) * a.inv_tau - norm + lse);
+                                      : p[b] * (ds_log_share(a, x[b], norm) -
+                                                ds_log_share(a, z[b], lse));
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, o);
         if (lane == 0) {
           a.loss[row] = w == 0.f ? 0.f
                                  : static_cast<float>(static_cast<double>(w) * a.tau * a.tau * loss);
-          if (a.lse) a.lse[row] = static_cast<float>(lse);
+          if (a.lse) a.lse[row] = static_cast<float>(lse.total());
         }
       }
       mbar_wait(&stored[turn], parity, aborted, err, DEV_ERR_EPI_WAIT);

@@ -147,3 +147,76 @@ def test_close_logits_at_a_small_temperature(K, n, v, dtype):
     assert bool(((lse.double() - wlse).abs() <= rel + U32 * wlse.abs()).all())
     for got in (loss, alone):
         assert bool(((got.double() - wl).abs() <= tau * tau * 12 * rel + U32 * wl.abs()).all())
+
+
+def relative(z, ids, t, tau):
+    """(loss, q, gradient) of rows however large their logits are: everything as a difference to the
+    row's, or the list's, maximum."""
+    u = (z.double() - z.double().amax(1, keepdim=True)) / tau
+    logs = u.exp().sum(1, keepdim=True).log()
+    c = t.double() - t.double().amax(1, keepdim=True)
+    logp = torch.log_softmax(c / tau, 1)
+    p = logp.exp()
+    at = ids.long()
+    q = (u - logs).exp()
+    loss = tau * tau * (p * (logp - (u - logs).gather(1, at))).sum(1)
+    return loss, q, tau * (q - torch.zeros_like(q).scatter_add_(1, at, p))
+
+
+@pytest.mark.parametrize("n,v,dtype", RING + FEW)
+@pytest.mark.parametrize("value", [-1e7, -1e12, -1e30, 1e12, -2e38, "lowest"])
+def test_rows_of_one_large_value(K, n, v, dtype, value):
+    """Rows, and lists, that hold nothing but one large finite value (a mask of -1e30, say): q = 1 / V,
+    p = 1 / k, loss = log V - log k."""
+    k, tau = 20, 0.75
+    if value == "lowest":
+        value = torch.finfo(dtype).min
+    z, ids, t = inputs(n, v, k, dtype, v + 3)
+    # the loss of a row is a difference of 1e-7 |value| or less only where all entries are alike
+    hit = torch.arange(n, device="cuda") % 3 == 1
+    both = torch.arange(n, device="cuda") % 6 == 4
+    z[hit] = value
+    t[both] = value
+    loss, lse, dz = run(K, z, ids, t, tau)
+    alone = torch.empty(n, device="cuda")
+    K.kronq_distill(z, ids, t, alone, temperature=tau)
+    torch.cuda.synchronize()
+    wl, q, wg = relative(z, ids, t, tau)
+    stat = (v / 256 + 64) * 2.0 ** -23
+    # an entry's exponent is below 32 here, log p and log q below 40, p and the mass good to stat
+    rel = stat + 64 * U32
+    size = tau * (2 * q + wg.abs() / tau)
+    assert bool(((dz.double() - wg).abs() <= rel * size + HALF[dtype] * wg.abs() + 1e-38).all())
+    for got in (loss, alone):
+        assert bool(((got.double() - wl).abs() <= tau * tau * 80 * rel + U32 * wl.abs()).all())
+    top = z[hit].double().amax(1) / tau
+    if abs(value) / tau > torch.finfo(F32).max:        # past fp32, which rounds it to an infinity
+        assert bool((lse[hit] == math.copysign(math.inf, value)).all())
+    else:
+        assert bool(((lse[hit].double() - top - math.log(v)).abs() <= stat + 2 * U32 * top.abs()).all())
+    assert K.kronq_device_error() == 0
+
+
+@pytest.mark.parametrize("n,v,dtype", [c for c in RING + FEW if c[2] == F32])
+@pytest.mark.parametrize("middle", [2.0 ** 20, -2.0 ** 20, 3e6, -4e7])
+def test_maxima_of_every_size(K, n, v, dtype, middle):
+    """Entries within a few tau of each other whose z / tau lies around 2^20 and beyond, where the
+    kernels change the form of the exponent: maxima of either form meet in a row's sum."""
+    k, tau = 6, 0.75
+    g = torch.Generator(device="cuda")
+    g.manual_seed(v)
+    z = torch.full((n, v), -3e38, device="cuda")
+    at = torch.randint(0, v // 12, (n, 12), generator=g, device="cuda") + torch.arange(
+        12, device="cuda") * (v // 12)
+    near = middle * tau * math.log(2.0)                # z c = middle
+    z.scatter_(1, at, near + torch.randint(-4, 5, (n, 12), generator=g, device="cuda").float() / 2)
+    ids = at[:, :k].to(torch.int32)
+    t = near + torch.randint(-4, 5, (n, k), generator=g, device="cuda").float() / 2
+    loss, lse, dz = run(K, z, ids, t, tau)
+    wl, q, wg = relative(z, ids, t, tau)
+    # exponents below 8, a dozen terms: the sums' joins and the exponentials
+    rel = 96 * 2.0 ** -23
+    p = torch.softmax((t.double() - near) / tau, 1)
+    size = tau * (2 * q + torch.zeros_like(q).scatter_add_(1, at[:, :k], p))
+    assert bool(((dz.double() - wg).abs() <= rel * size + U32 * wg.abs() + 1e-38).all())
+    assert bool(((loss.double() - wl).abs() <= tau * tau * 20 * rel + U32 * wl.abs()).all())
