@@ -220,3 +220,85 @@ def test_maxima_of_every_size(K, n, v, dtype, middle):
     size = tau * (2 * q + torch.zeros_like(q).scatter_add_(1, at[:, :k], p))
     assert bool(((dz.double() - wg).abs() <= rel * size + U32 * wg.abs() + 1e-38).all())
     assert bool(((loss.double() - wl).abs() <= tau * tau * 20 * rel + U32 * wl.abs()).all())
+
+
+@pytest.mark.parametrize("n,v,dtype", RING + FEW)
+def test_in_place(K, n, v, dtype):
+    """dlogits = logits, with entries of every CTA's part of the row listed: the bits of a gradient of its
+    own, and those near the definition's. The teacher's logits are fp32 beside either type."""
+    k, tau = 64, 1.25
+    z, ids, t = inputs(n, v, k, dtype, v + 4)
+    ids[1::5, 3] = ids[1::5, 40]                       # listed twice
+    w = 0.5 + torch.rand(n, device="cuda")
+    loss, lse, dz = run(K, z, ids, t, tau, w)
+    for _ in range(5):
+        zc = z.clone()
+        loss2, lse2, _ = run(K, zc, ids, t, tau, w, dz=zc)
+        assert torch.equal(loss, loss2) and torch.equal(lse, lse2) and torch.equal(dz, zc)
+    back, zc = torch.empty_like(z), z.clone()
+    K.kronq_distill_backward(z, ids, t, lse, w, back, temperature=tau)
+    K.kronq_distill_backward(zc, ids, t, lse, w, zc, temperature=tau)
+    torch.cuda.synchronize()
+    assert torch.equal(back, zc)
+    stat = (v / 256 + 64) * 2.0 ** -23
+    for r in range(0, n, 100):
+        s = slice(r, r + 100)
+        wl, wlse, q, wg = exact(z[s], ids[s], t[s], tau, w[s])
+        unit = w[s].double()[:, None] * tau
+        size = 2 * unit * q + wg.abs()
+        tol = (stat + 100 * U32) * size + HALF[dtype] * wg.abs() + 1e-38
+        assert bool(((dz[s].double() - wg).abs() <= tol).all())
+        # from the rounded lse: 2^-24 of it more in the exponent
+        tol = tol + 2 * U32 * wlse.abs()[:, None] * size
+        assert bool(((back[s].double() - wg).abs() <= tol).all())
+        assert bool(((loss[s].double() - wl).abs() <= w[s] * tau * tau * 40 * (stat + 100 * U32)
+                     + U32 * wl.abs()).all())
+    assert K.kronq_device_error() == 0
+
+
+@pytest.mark.parametrize("n,v,dtype", RING + FEW)
+def test_masked_rows(K, n, v, dtype):
+    """Rows of every kind beside each other: masks of -inf and of the type's lowest value around the
+    list, nothing left, an entry masked, weight 0, no entries, entries without probability."""
+    k, tau = 20, 1.0
+    z, ids, t = inputs(n, v, k, dtype, v + 5)
+    w = 0.5 + torch.rand(n, device="cuda")
+    kind = torch.arange(n, device="cuda") % 10 if n >= 10 else torch.arange(n, device="cuda") * 2 + 1
+    listed = torch.zeros(n, v, dtype=torch.bool, device="cuda").scatter_(1, ids.long(), True)
+    for at, value in ((1, -math.inf), (2, torch.finfo(dtype).min)):
+        z.masked_fill_((kind == at)[:, None] & ~listed, value)
+    z[kind == 3] = -math.inf
+    hide = kind == 4
+    z[hide, ids[hide, 7].long()] = -math.inf
+    w[kind == 5] = 0.0
+    z[kind == 5, 11] = math.nan
+    z[kind == 5, v - 1] = math.inf
+    ids[kind == 6] = -1
+    t[kind == 6] = math.nan                            # absent: not looked at
+    t[kind == 7, 2:] = -math.inf
+    ids[kind == 8, 5:] = v                             # outside
+    del listed
+    loss, lse, dz = run(K, z, ids, t, tau, w)
+    none = (kind == 5) | (kind == 6)
+    assert bool((loss[none] == 0).all()) and bool((dz[none] == 0).all())
+    assert bool((loss[(kind == 3) | hide] == math.inf).all()) and bool((lse[kind == 3] == -math.inf).all())
+    stat = (v / 256 + 64) * 2.0 ** -23
+    # nothing left: q = 0, the gradient is -w p alone
+    rows = kind == 3
+    p = torch.softmax(t[rows].double(), 1)
+    want = torch.zeros_like(dz[rows], dtype=torch.float64).scatter_(1, ids[rows].long(),
+                                                                     -w[rows].double()[:, None] * p)
+    tol = (stat + 100 * U32 + HALF[dtype]) * want.abs()
+    assert bool(((dz[rows].double() - want).abs() <= tol).all())
+    ids = ids.masked_fill(ids >= v, -1)
+    t = t.masked_fill((kind == 6)[:, None], 0.0)
+    rows = ~(none | (kind == 3))
+    z, ids, t, w, loss, lse, dz, hide = (c[rows] for c in (z, ids, t, w, loss, lse, dz, hide))
+    wl, wlse, q, wg = exact(z, ids, t, tau, w)
+    unit = w.double()[:, None] * tau
+    tol = (stat + 100 * U32) * (2 * unit * q + wg.abs()) + HALF[dtype] * wg.abs() + 1e-38
+    assert bool(((dz.double() - wg).abs() <= tol).all())
+    assert bool(((lse.double() - wlse).abs() <= stat + 2 * U32 * wlse.abs()).all())
+    off = (loss.double() - wl).abs() <= w * 40 * (stat + 100 * U32) + U32 * wl.abs()
+    assert bool((off | hide).all())
+    assert K.kronq_device_error() == 0
