@@ -7,6 +7,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <initializer_list>
 #include <mutex>
 #include <vector>
 
@@ -170,6 +171,13 @@ kronq_status check_byte_matrix(const void* p, int64_t* ld, int64_t rows, int64_t
   return KRONQ_OK;
 }
 
+// fp32 and int32 vectors (NULL passes).
+kronq_status check_words(std::initializer_list<const void*> vectors, const char* names) {
+  for (const void* p : vectors)
+    if (!aligned(p, 4)) return fail(KRONQ_ERR_INVALID_ARG, "%s: not 4-byte aligned", names);
+  return KRONQ_OK;
+}
+
 kronq_status check_quant_tokens(const void* x, int32_t x_dtype, int64_t ld_x, int32_t n_tok,
                                 int32_t d_in, const float* s_x, const int8_t* sign_in,
                                 uint32_t flags) {
@@ -177,6 +185,7 @@ kronq_status check_quant_tokens(const void* x, int32_t x_dtype, int64_t ld_x, in
   if ((flags & KRONQ_BIIP_SCALE_IN) && !s_x) return fail(KRONQ_ERR_INVALID_ARG, "s_x is NULL");
   if ((flags & KRONQ_BIIP_ROTATE_IN) && !sign_in)
     return fail(KRONQ_ERR_INVALID_ARG, "sign_in is NULL");
+  if (flags & KRONQ_BIIP_SCALE_IN) KQ_TRY(check_words({s_x}, "s_x"));
   if (d_in > kMaxI8Width)
     return fail(KRONQ_ERR_UNSUPPORTED, "d_in = %d exceeds %d", d_in, kMaxI8Width);
   if ((flags & KRONQ_BIIP_ROTATE_IN) && d_in > kMaxRotatedWidth)
@@ -191,8 +200,7 @@ kronq_status check_codes(const void* codes, int32_t codes_dtype, int64_t* ld_cod
     return fail(KRONQ_ERR_INVALID_ARG, "codes_dtype must be KRONQ_DTYPE_U8 or KRONQ_DTYPE_S8");
   KQ_TRY(check_byte_matrix(codes, ld_codes, d_out, d_in, "codes"));
   if (!scale) return fail(KRONQ_ERR_INVALID_ARG, "scale is NULL");
-  if (!aligned(scale, 4) || !aligned(zero, 4))
-    return fail(KRONQ_ERR_INVALID_ARG, "scale or zero not 4-byte aligned");
+  KQ_TRY(check_words({scale, zero}, "scale or zero"));
   if (d_in > kMaxI8Width)
     return fail(KRONQ_ERR_UNSUPPORTED, "d_in = %d exceeds %d", d_in, kMaxI8Width);
   return KRONQ_OK;
@@ -221,7 +229,8 @@ kronq_status check_distill(const void* logits, int32_t logits_dtype, int64_t ld_
                            const int32_t* ids, int64_t ld_ids, const void* top, int32_t top_dtype,
                            int64_t ld_top, int32_t n_tok, int32_t vocab, int32_t k,
                            float temperature, const void* dlogits, int32_t dlogits_dtype,
-                           int64_t ld_dlogits) {
+                           int64_t ld_dlogits, std::initializer_list<const void*> rows) {
+  KQ_TRY(check_words(rows, "a vector of one value per row"));
   KQ_TRY(check_float_matrix(logits, logits_dtype, ld_logits, n_tok, vocab, "logits"));
   if (vocab > (1 << 30)) return fail(KRONQ_ERR_UNSUPPORTED, "vocab = %d exceeds 2^30", vocab);
   if (k > kMaxDistillTop)
@@ -628,6 +637,7 @@ kronq_status kronq_quantize_tokens(const void* x, int32_t x_dtype, int64_t ld_x,
   KQ_TRY(check_byte_matrix(q, &ld_q, n_tok, d_in, "q"));
   if (!tok_scale || !tok_sum)
     return fail(KRONQ_ERR_INVALID_ARG, "tok_scale and tok_sum are required");
+  KQ_TRY(check_words({tok_scale, tok_sum}, "tok_scale or tok_sum"));
   KQ_TRY(kronq_device_check());
   const QuantTokensArgs a{x, x_dtype, ld_x, n_tok, d_in,
                           (flags & KRONQ_BIIP_SCALE_IN) ? s_x : nullptr,
@@ -648,6 +658,7 @@ kronq_status kronq_matmul_i8(const int8_t* q, int64_t ld_q, const float* tok_sca
   KQ_TRY(check_byte_matrix(q, &ld_q, n_tok, d_in, "q"));
   if (!tok_scale) return fail(KRONQ_ERR_INVALID_ARG, "tok_scale is NULL");
   if (zero && !tok_sum) return fail(KRONQ_ERR_INVALID_ARG, "tok_sum is NULL (zero needs it)");
+  KQ_TRY(check_words({tok_scale, tok_sum}, "tok_scale or tok_sum"));
   KQ_TRY(check_float_matrix(y, y_dtype, ld_y, n_tok, d_out, "y"));
   KQ_TRY(kronq_device_check());
   const I8MatmulArgs a{q, ld_q, tok_scale, tok_sum, n_tok, codes, ld_codes,
@@ -676,6 +687,7 @@ kronq_status kronq_qlinear8(const void* x, int32_t x_dtype, int64_t ld_x, int32_
   KQ_TRY(check_quant_tokens(x, x_dtype, ld_x, n_tok, d_in, s_x, sign_in, flags));
   KQ_TRY(check_codes(codes, codes_dtype, &ld_codes, scale, zero, d_out, d_in));
   if ((flags & KRONQ_BIIP_SCALE_OUT) && !s_g) return fail(KRONQ_ERR_INVALID_ARG, "s_g is NULL");
+  if (flags & KRONQ_BIIP_SCALE_OUT) KQ_TRY(check_words({s_g}, "s_g"));
   const bool rot_out = (flags & KRONQ_BIIP_ROTATE_OUT) != 0;
   if (rot_out && !sign_out) return fail(KRONQ_ERR_INVALID_ARG, "sign_out is NULL");
   if (rot_out && (d_out & -d_out) > kMaxOutBlock)
@@ -727,7 +739,8 @@ kronq_status kronq_distill(const void* logits, int32_t logits_dtype, int64_t ld_
     return fail(KRONQ_ERR_SHAPE, "vocab must be positive, n_tok and k >= 0");
   if (n_tok == 0) return KRONQ_OK;
   KQ_TRY(check_distill(logits, logits_dtype, ld_logits, ids, ld_ids, top, top_dtype, ld_top, n_tok,
-                       vocab, k, temperature, dlogits, dlogits_dtype, ld_dlogits));
+                       vocab, k, temperature, dlogits, dlogits_dtype, ld_dlogits,
+                       {loss, lse, top_lse, row_weight}));
   if (!loss) return fail(KRONQ_ERR_INVALID_ARG, "loss is NULL");
   KQ_TRY(kronq_device_check());
   const DistillArgs a{logits, logits_dtype, ld_logits, ids, ld_ids, top, top_dtype, ld_top,
@@ -749,7 +762,8 @@ kronq_status kronq_distill_backward(const void* logits, int32_t logits_dtype, in
   if (!lse || !dloss || !dlogits)
     return fail(KRONQ_ERR_INVALID_ARG, "lse, dloss and dlogits are required");
   KQ_TRY(check_distill(logits, logits_dtype, ld_logits, ids, ld_ids, top, top_dtype, ld_top, n_tok,
-                       vocab, k, temperature, dlogits, dlogits_dtype, ld_dlogits));
+                       vocab, k, temperature, dlogits, dlogits_dtype, ld_dlogits,
+                       {lse, dloss, top_lse}));
   KQ_TRY(kronq_device_check());
   const DistillArgs a{logits, logits_dtype, ld_logits, ids, ld_ids, top, top_dtype, ld_top,
                       n_tok, vocab, k, top_lse, dloss, temperature, lse, nullptr, nullptr,
