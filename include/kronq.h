@@ -440,7 +440,8 @@ KRONQ_API kronq_status kronq_quantize_tokens(const void* x, int32_t x_dtype, int
  *            may be NULL (no zero point, symmetric codes)
  *   y        (device) n_tok x d_out, y_dtype KRONQ_DTYPE_F32 or KRONQ_DTYPE_BF16, row stride ld_y
  *            elements (>= d_out), aligned to its element size
- *   d_in <= 65536 (the int32 sums are then exact). n_tok = 0 is a no-op. No workspace.
+ *   d_in <= 65536 (the int32 sums are then exact); n_tok and d_out <= 2^31 - 256
+ *   (KRONQ_ERR_UNSUPPORTED). n_tok = 0 is a no-op. No workspace.
  *   Under an SM budget the CTAs work in pairs: an even number of them, and two at least.
  *   Arithmetic: the integer sum and its zero-point correction are exact (for a zero that is no
  *   whole number, or so large that int32 could not hold the result, in fp64); it is rounded to

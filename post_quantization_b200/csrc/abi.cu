@@ -194,6 +194,13 @@ kronq_status check_quant_tokens(const void* x, int32_t x_dtype, int64_t ld_x, in
   return KRONQ_OK;
 }
 
+// Tiles of up to 256 channels by 256 tokens are counted in 32 bits.
+kronq_status check_matmul_sizes(int32_t n_tok, int32_t d_out) {
+  if (std::max(n_tok, d_out) > kMaxI8Rows)
+    return fail(KRONQ_ERR_UNSUPPORTED, "n_tok or d_out exceeds %d", kMaxI8Rows);
+  return KRONQ_OK;
+}
+
 kronq_status check_codes(const void* codes, int32_t codes_dtype, int64_t* ld_codes,
                          const float* scale, const float* zero, int32_t d_out, int32_t d_in) {
   if (codes_dtype != KRONQ_DTYPE_U8 && codes_dtype != KRONQ_DTYPE_S8)
@@ -654,6 +661,7 @@ kronq_status kronq_matmul_i8(const int8_t* q, int64_t ld_q, const float* tok_sca
   if (d_out <= 0 || d_in <= 0 || n_tok < 0)
     return fail(KRONQ_ERR_SHAPE, "d_out, d_in must be positive and n_tok >= 0");
   if (n_tok == 0) return KRONQ_OK;
+  KQ_TRY(check_matmul_sizes(n_tok, d_out));
   KQ_TRY(check_codes(codes, codes_dtype, &ld_codes, scale, zero, d_out, d_in));
   KQ_TRY(check_byte_matrix(q, &ld_q, n_tok, d_in, "q"));
   if (!tok_scale) return fail(KRONQ_ERR_INVALID_ARG, "tok_scale is NULL");
@@ -684,6 +692,7 @@ kronq_status kronq_qlinear8(const void* x, int32_t x_dtype, int64_t ld_x, int32_
   if (flags & ~static_cast<uint32_t>(KRONQ_BIIP_FULL))
     return fail(KRONQ_ERR_INVALID_ARG, "flags may only hold the four transform bits");
   if (n_tok == 0) return KRONQ_OK;
+  KQ_TRY(check_matmul_sizes(1, d_out));      // tokens are taken in passes
   KQ_TRY(check_quant_tokens(x, x_dtype, ld_x, n_tok, d_in, s_x, sign_in, flags));
   KQ_TRY(check_codes(codes, codes_dtype, &ld_codes, scale, zero, d_out, d_in));
   if ((flags & KRONQ_BIIP_SCALE_OUT) && !s_g) return fail(KRONQ_ERR_INVALID_ARG, "s_g is NULL");

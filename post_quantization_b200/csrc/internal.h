@@ -121,6 +121,7 @@ struct I8MatmulArgs {
   int after_quant, before_transform;   // launched between the layer's other two kernels
 };
 constexpr int kMaxI8Width = 65536;     // 128 * 255 * 65536 < 2^31
+constexpr int kMaxI8Rows = INT32_MAX - 255;   // the last tile ends within int32
 kronq_status run_i8matmul(const I8MatmulArgs& a, cudaStream_t stream);
 
 // tokquant.cu: per-token 8-bit activations (with the input transforms) and the output transforms.

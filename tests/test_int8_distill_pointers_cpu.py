@@ -61,3 +61,15 @@ def test_vectors_off_alignment(K, name):
         at = call[2][call[1].index(vector)]
         for off in (1, 2, 3):
             assert status(call, **{vector: at + off}) == K.ERR_INVALID_ARG, (vector, off)
+
+
+@pytest.mark.parametrize("name", ["matmul_i8", "qlinear8"])
+def test_sizes_whose_last_tile_passes_32_bits(K, name):
+    """A tile of 256 channels or tokens from there on would end past 2^31 - 1."""
+    call = calls(K)[name]
+    most = 2 ** 31 - 256
+    wide = {"ld_y": 2 ** 31, "wsb": 2 ** 62, "flags": 0}
+    tokens = [] if name == "qlinear8" else [(32, most + 1), (32, 2 ** 31 - 1)]   # that takes passes
+    for d_out, n in [(most + 1, 2), (2 ** 31 - 1, 2)] + tokens:
+        changed = {k: v for k, v in {**wide, "d_out": d_out, "n": n}.items() if k in call[1]}
+        assert status(call, **changed) == K.ERR_UNSUPPORTED, (d_out, n)
