@@ -30,18 +30,29 @@ class SublayerResult:
     w_hat: torch.Tensor | None = None
 
 
+def _capturing(t: torch.Tensor) -> bool:
+    return t.is_cuda and torch.cuda.is_current_stream_capturing()
+
+
 class Workspace:
-    """One device scratch buffer, grown on demand and reused by every call on one stream."""
+    """One device scratch buffer, grown on demand and reused by every call on one stream.
+
+    A buffer that a CUDA graph was captured with is kept as long as the workspace, also when it has
+    grown past it: replays write there. Graphs that share a workspace are replayed on one stream.
+    """
 
     def __init__(self, device):
         self.device = device
         self.buf = torch.empty(0, dtype=torch.uint8, device=device)
+        self.captured = []
 
     def get(self, nbytes: int):
         if nbytes == 0:
             return None
         if self.buf.numel() < nbytes + 256:
             self.buf = torch.empty(nbytes + 256, dtype=torch.uint8, device=self.device)
+        if _capturing(self.buf) and not (self.captured and self.captured[-1] is self.buf):
+            self.captured.append(self.buf)
         off = (-self.buf.data_ptr()) % 256
         return self.buf[off:off + nbytes]
 
