@@ -69,6 +69,30 @@ kronq_status check_launch(const char* what) {
   return KRONQ_OK;
 }
 
+kronq_status raise_smem(const void* kern, size_t bytes) {
+  struct Limit {
+    const void* kern;
+    int dev;
+    size_t bytes;
+  };
+  static std::mutex mu;
+  static Limit known[256];
+  static int count = 0;
+  int dev = 0;
+  KQ_CUDA_TRY(cudaGetDevice(&dev));
+  std::lock_guard<std::mutex> lock(mu);
+  int i = 0;
+  while (i < count && (known[i].kern != kern || known[i].dev != dev)) ++i;
+  if (i < count && known[i].bytes >= bytes) return KRONQ_OK;
+  KQ_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   static_cast<int>(bytes)));
+  if (i < 256) {                 // far more than the library's kernels on a machine's devices
+    known[i] = {kern, dev, bytes};
+    count = std::max(count, i + 1);
+  }
+  return KRONQ_OK;
+}
+
 kronq_status encode_tiled_map(CUtensorMap* map, CUtensorMapDataType dtype, int rank,
                               const void* base, const uint64_t* dims, const uint64_t* strides,
                               const uint32_t* box, CUtensorMapSwizzle swizzle) {

@@ -904,8 +904,7 @@ kronq_status row_pass_tile(const T* src, float* dst, int64_t rows, int64_t cols,
   const int64_t rb = log2b >= 12 ? 1 : 4096 / b;
   const int64_t nchunks = (cols / b) * ((rows + rb - 1) / rb);
   auto launch = [&](auto kern, int nt, size_t smem) -> kronq_status {
-    KQ_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     static_cast<int>(smem)));
+    KQ_TRY(raise_smem(reinterpret_cast<const void*>(kern), smem));
     int per_sm = 1;   // the CTAs that fit at once; each takes a contiguous range of chunks
     KQ_CUDA_TRY(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, nt, smem));
     if (per_sm < 1) per_sm = 1;
@@ -1045,8 +1044,7 @@ kronq_status col_pass_tma(float* m, int64_t rows, int64_t cols, int log2p, int r
   const int64_t ncg = ((cols + 31) / 32 + ct - 1) / ct;
   const int64_t nchunks = (rows / P) * ncg;
   auto launch = [&](auto kern, int nt, size_t smem) -> kronq_status {
-    KQ_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     static_cast<int>(smem)));
+    KQ_TRY(raise_smem(reinterpret_cast<const void*>(kern), smem));
     int per_sm = 1;   // the CTAs that fit at once; each takes a contiguous range of chunks
     KQ_CUDA_TRY(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, nt, smem));
     if (per_sm < 1) per_sm = 1;
@@ -1097,8 +1095,7 @@ kronq_status row_pass(const T* src, float* dst, int64_t rows, int64_t cols, cons
     // grid is the CTAs that fit at once (each walks chunks grid-stride)
     auto launch = [&](auto kern) -> kronq_status {
       if (smem > 48 * 1024)
-        KQ_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem));
+        KQ_TRY(raise_smem(reinterpret_cast<const void*>(kern), smem));
       int per_sm = 1;
       KQ_CUDA_TRY(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem));
       if (per_sm < 1) per_sm = 1;
@@ -1118,8 +1115,7 @@ kronq_status row_pass(const T* src, float* dst, int64_t rows, int64_t cols, cons
   }
   const size_t smem = static_cast<size_t>(chunk) * sizeof(float);
   if (smem > 48 * 1024)
-    KQ_CUDA_TRY(cudaFuncSetAttribute(fwht_rows_kernel<T>,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+    KQ_TRY(raise_smem(reinterpret_cast<const void*>(fwht_rows_kernel<T>), smem));
   fwht_rows_kernel<T><<<static_cast<unsigned>(blocks), 256, smem, stream>>>(
       src, dst, rows, cols, row_f, col_f, scalar, ilog2_pow2(b), chunk, out_scale);
   return check_launch("fwht_rows_kernel");
@@ -1135,8 +1131,7 @@ kronq_status col_pass_reg(float* m, int64_t rows, int64_t cols, int log2p, int r
   const int64_t tiles = ((cols + kColTile - 1) / kColTile) * (rows / P);
   auto launch = [&](auto kern) -> kronq_status {
     if (smem > 48 * 1024)
-      KQ_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem)));
+      KQ_TRY(raise_smem(reinterpret_cast<const void*>(kern), smem));
     int per_sm = 1;   // the CTAs that fit at once; each walks tiles grid-stride
     KQ_CUDA_TRY(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, 2 * P, smem));
     if (per_sm < 1) per_sm = 1;
@@ -1179,8 +1174,7 @@ kronq_status col_pass(float* m, int64_t rows, int64_t cols, int b, cudaStream_t 
   if (cw < 1) cw = 1;
   const size_t smem = static_cast<size_t>(b) * cw * sizeof(float);
   if (smem > 48 * 1024)
-    KQ_CUDA_TRY(cudaFuncSetAttribute(fwht_cols_kernel,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+    KQ_TRY(raise_smem(reinterpret_cast<const void*>(fwht_cols_kernel), smem));
   dim3 grid(static_cast<unsigned>((cols + cw - 1) / cw), static_cast<unsigned>(rows / b));
   fwht_cols_kernel<<<grid, 256, smem, stream>>>(m, rows, cols, ilog2_pow2(b), cw, out_scale);
   return check_launch("fwht_cols_kernel");

@@ -218,6 +218,10 @@ inline kronq_status allow_smem(const void* kern, size_t bytes, std::atomic<uint6
   return KRONQ_OK;
 }
 
+// The same for a kernel whose launches take different amounts: raises its limit to `bytes` where it is
+// lower. Never lowers it: launches of other host threads may count on it.
+kronq_status raise_smem(const void* kern, size_t bytes);
+
 // Launches a kernel that may start while the one before it on the stream still runs (programmatic
 // dependent launch); it waits (griddepcontrol.wait) before it touches what that kernel reads or
 // writes. cluster: CTAs per cluster along x.

@@ -1335,18 +1335,14 @@ QlGeom ql_geom(int d_out, int d_in, int n_tok_pass) {
 template <int BITS, int NTC>
 kronq_status launch_mma_t(const QlMmaArgs& p, int C, size_t smem, cudaStream_t stream) {
   auto kern = qlin_mma_kernel<BITS, NTC>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(smem));
-  if (e != cudaSuccess) return fail(KRONQ_ERR_CUDA, "qlin_mma smem: %s", cudaGetErrorString(e));
+  KQ_TRY(raise_smem(reinterpret_cast<const void*>(kern), smem));
   return launch_pdl(kern, dim3(C), dim3(QL_THREADS), smem, stream, true, "qlin_mma_kernel", p);
 }
 
 template <int BITS, int NT>
 kronq_status launch_dp_t(const QlDpArgs& p, int C, size_t smem, cudaStream_t stream) {
   auto kern = qlin_dp4a_kernel<BITS, NT>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(smem));
-  if (e != cudaSuccess) return fail(KRONQ_ERR_CUDA, "qlin_dp4a smem: %s", cudaGetErrorString(e));
+  KQ_TRY(raise_smem(reinterpret_cast<const void*>(kern), smem));
   return launch_pdl(kern, dim3(C), dim3(QL_DP_THREADS), smem, stream, true, "qlin_dp4a_kernel", p);
 }
 
@@ -1443,8 +1439,7 @@ kronq_status run_qlinear(const QlinearArgs& q, void* ws, cudaStream_t stream) {
   }
   const int in_threads = std::max(32, span / 4);
   const size_t in_smem = static_cast<size_t>(2 * (span + span / 16)) * sizeof(float);
-  KQ_CUDA_TRY(cudaFuncSetAttribute(qlin_in_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   static_cast<int>(in_smem)));
+  KQ_TRY(raise_smem(reinterpret_cast<const void*>(qlin_in_kernel), in_smem));
   const int qb = (rot_out && b_out > QL_TILE) ? b_out / QL_TILE : 1;
   const size_t out_smem = static_cast<size_t>(qb) * (16 * sizeof(float) + 2 * sizeof(int));
 

@@ -91,3 +91,33 @@ def test_lists_of_several_lengths(K):
     torch.cuda.synchronize()
     side_by_side(K, jobs, 4000)
     assert all(torch.equal(a, b) for w, g in zip(want, got) for a, b in zip(w, g))
+
+
+def test_packed_layers_of_several_widths(K):
+    """kronq_qlinear: its kernels' shared memory goes by the layer's width and the token count."""
+    fn = K.load_library().kronq_qlinear
+    got, want, jobs, keep = [], [], [], []
+    for d_in, n in ((1024, 1), (4096, 4), (8192, 2), (11008, 3), (2048, 8), (28672, 1)):
+        d_out, tag = 256, ("threads", d_in)
+        packed = K.kronq_pack_codes(synth.codes(d_out, d_in, 2, synth.seed_for(tag, "c"), device="cuda"), 2)
+        scale, zero = synth.grid_params(d_out, 0, 2, synth.seed_for(tag, "g"), device="cuda")
+        grid = K.kronq_pack_grid(scale, zero, d_out, d_in, 0)
+        s_x = synth.positive_scales(d_in, synth.seed_for(tag, "sx"), device="cuda")
+        s_g = synth.positive_scales(d_out, synth.seed_for(tag, "sg"), device="cuda")
+        si = synth.rademacher(d_in, synth.seed_for(tag, "si"), device="cuda")
+        so = synth.rademacher(d_out, synth.seed_for(tag, "so"), device="cuda")
+        x = synth.activations(n, d_in, synth.seed_for(tag, "x"), dtype=torch.bfloat16, device="cuda")
+        ys = [torch.zeros(n, d_out, device="cuda") for _ in range(2)]
+        K.kronq_qlinear(x, packed, grid, s_x, s_g, si, so, K.BIIP_FULL, d_out, 2, ys[0])
+        want.append(ys[0])
+        got.append(ys[1])
+        size = K.kronq_qlinear_workspace_size(d_out, d_in, n)
+        ws = torch.empty(size + 256, dtype=torch.uint8, device="cuda")
+        ws = ws[-ws.data_ptr() % 256:][:size]
+        keep.append((packed, grid, s_x, s_g, si, so, x, ws))
+        jobs.append((fn, (x.data_ptr(), K.DTYPE_BF16, d_in, n, packed.data_ptr(), grid.data_ptr(), 0,
+                          s_x.data_ptr(), s_g.data_ptr(), si.data_ptr(), so.data_ptr(), K.BIIP_FULL,
+                          d_out, d_in, 2, ys[1].data_ptr(), d_out, ws.data_ptr(), size)))
+    torch.cuda.synchronize()
+    side_by_side(K, jobs, 4000)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
