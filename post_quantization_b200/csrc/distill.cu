@@ -1025,8 +1025,8 @@ __global__ void __launch_bounds__(DS_RING_THREADS, 2)
   }
 }
 
-// Loss and gradient; NV vectors of z per thread stay in registers. 96 x 50001 bf16: 9.3 us of the GPU,
-// the launch, one read and the barriers' latency; 256 x 128256: 44 us, 3 TB/s.
+// Loss and gradient; NV vectors of z per thread stay in registers. 96 x 50001 bf16: 8.6 us of the GPU,
+// the launch, one read and the barriers' latency; 256 x 128256: 40 us, 3.3 TB/s.
 template <typename T, typename D, int NV, int KPT>
 __global__ void __launch_bounds__(DS_THREADS, NV > 8 ? 2 : (KPT == 1 ? 4 : 3)) distill_hold_kernel(DsArgs a) {
   __shared__ DsShared sh;

@@ -475,8 +475,9 @@ __device__ __forceinline__ float4 tq_load4(const __nv_bfloat16* p, int j0, uint3
 }
 
 // Tokens whose Hadamard blocks are above 8: one CTA per token, which holds the row in shared memory.
-// Bound by instructions (about 33 a warp for 32 elements, 57 % of the issue slots): 2048 x 8192 bf16 in
-// 31 us, 1.6 TB/s. With 8 neighbours a thread and four passes it took 38.5 us.
+// Bound by the latency of a row's steps, one behind the other, and by instructions (about 37 a warp for 32
+// elements, 64 % of the issue slots of active cycles): 2048 x 8192 bf16 in 30 us, 1.7 TB/s. With 8
+// neighbours a thread and four passes it took 38.5 us.
 template <typename T, bool VEC, int TOP>
 __global__ void __launch_bounds__(TQ_MAX_THREADS, TQ_CTAS) quant_rotated_kernel(QuantArgs a) {
   extern __shared__ __align__(16) float xs[];
