@@ -331,8 +331,9 @@ __global__ void __launch_bounds__(SP_THREADS, 2)
       tok[j] = make_float2(p.tok_scale[tn * BN + j],
                            __int_as_float(p.tok_sum ? p.tok_sum[tn * BN + j] : 0));
   __syncwarp();
-  const bool ok = mbar_wait(done, 0, abort_flag, p.err, DEV_ERR_EPI_WAIT);
-  __syncthreads();     // every role has left its loop; the MMAs and the copies they used are done
+  // every role has left its loop; the MMAs and the copies they used are done, or all threads skip the
+  // accumulator (its loads are for whole warps)
+  const bool ok = __syncthreads_and(mbar_wait(done, 0, abort_flag, p.err, DEV_ERR_EPI_WAIT)) != 0;
   tc_fence_after();
   const int q = warp & 3, half = warp >> 2;
   const uint32_t taddr = tmem_base + ((q * 32u) << 16);
